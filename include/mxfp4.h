@@ -379,6 +379,83 @@ typedef struct {
 
 int grouped_gemm_nvfp4(const nvfp4_group* groups, int G, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The 8-bit integer path: int8 codes with one fp32 scale per row (token) of an
+ * activation and per row (output channel) of a weight, for layers that need
+ * more than 4 bits. The rule for one row of fp32 values y[0..K):
+ *   s    = max(fl(max_k |y[k]| * fl(1/127)), 2^-126),   r = fl(1/s),
+ *   q[k] = fl(y[k] * r) rounded to the nearest integer, ties to even,
+ * where fl rounds to fp32 (nearest even); |q[k]| <= 127 follows. y[k] is
+ * approximately q[k] * s. Unlike the calls above these define rows that are not
+ * finite: one that holds an Inf or a NaN gets s = NaN and q = 0.
+ * MXFP4_TYPE_*: the element type of a call's unquantised tensors; any other value
+ * gives MXFP4_ERR_ARG.
+ * ------------------------------------------------------------------------- */
+#define MXFP4_TYPE_BF16 0
+#define MXFP4_TYPE_F16 1
+#define MXFP4_TYPE_F32 2
+
+/* ---------------------------------------------------------------------------
+ * int8_quant -- the rule above on each row of X[M, K].
+ *   x : [M, K] of type `dtype`, row stride ldx elements (ldx >= K); x and the
+ *       stride in bytes must be multiples of 16.
+ *   q : out, int8 [M, K], row stride ldq bytes (ldq >= K); q and ldq multiples
+ *       of 16 bytes.
+ *   s : out, fp32 [M], 4-byte aligned.
+ *   M >= 1, K % 16 == 0, 16 <= K <= 2^28. No two of x, q and s may overlap.
+ * ------------------------------------------------------------------------- */
+int int8_quant(const void* x, int64_t ldx, int dtype, void* q, int64_t ldq, float* s, int64_t M, int64_t K,
+               void* stream);
+
+/* ---------------------------------------------------------------------------
+ * int8_rmsnorm_quant -- the residual's addition, the root-mean-square norm of
+ * the sum and its quantisation, in one launch, per row:
+ *   h   = x + residual, the fp32 sum rounded to `dtype` (h = x without one);
+ *   ss  = sum_k h[k]^2 in float64, added in one fixed order (the same result on
+ *         every run), within K * 2^-53 relative of the exact sum (bf16 and fp16
+ *         squares are exact);
+ *   inv = fp32(1 / sqrt(ss / K + eps)), float64 steps;
+ *   y   = fl(fl(h * inv) * w), kept in fp32, then the rule above.
+ *   x, residual, w, h : of type `dtype`. x, residual and h are [M, K] with row
+ *         strides in elements, w is [K]; each pointer and each stride in bytes
+ *         a multiple of 16.
+ *   residual, h : both NULL (no addition, their strides are not read) or both
+ *         given (else MXFP4_ERR_NULL). h may be x or residual itself (same
+ *         pointer and stride: the stream is updated in place); otherwise no
+ *         output may overlap any other argument.
+ *   eps : finite, > 0; otherwise MXFP4_ERR_ARG.
+ *   q, s, M, K : as for int8_quant.
+ * ------------------------------------------------------------------------- */
+int int8_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* w, float eps,
+                       int dtype, void* h, int64_t ldh, void* q, int64_t ldq, float* s, int64_t M, int64_t K,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gemm_a8w8 -- the product of two int8 matrices with a scale for each token (row
+ * of A) and output channel (row of B):
+ *   acc     = sum_k Aq[m, k] * Bq[n, k], exact in int32 (all 256 codes allowed);
+ *   C[m, n] = T(fl(fl(fl(acc) * as[m]) * bs[n])), with a bias
+ *             T(fl(fl(fl(fl(acc) * as[m]) * bs[n]) + bias[n])),
+ * T rounding to the type of C (nearest even; fp16 overflow gives infinity).
+ * The result depends on nothing but the operands: not on the kernel that a
+ * shape takes, and a row of C not on the other rows.
+ *   Aq : int8 [M, K], row stride lda bytes, K <= lda <= 2^22.
+ *   as : fp32 [M].
+ *   Bq : int8 [N, K] row-major (as int8_quant leaves a weight), row stride ldb
+ *        bytes, K <= ldb <= 2^22.
+ *   bs : fp32 [N].
+ *   bias : [N] of type ctype, or NULL.
+ *   C  : out, [M, N] of type ctype, row stride ldc elements, N <= ldc <= 2^36;
+ *        aligned to its element. No overlap with the operands.
+ *   Aq, lda, Bq, ldb : multiples of 16 bytes; as, bs 4-byte aligned, bias
+ *        aligned to its element.
+ *   M, N >= 1, M, N <= 2^24, ceil(M/16) * ceil(N/16) <= 2^30; K % 16 == 0,
+ *   16 <= K <= 131056 (the largest that keeps every acc in int32).
+ *   No workspace; operands are used where they are (no packing).
+ * ------------------------------------------------------------------------- */
+int gemm_a8w8(const void* Aq, int64_t lda, const float* as, const void* Bq, int64_t ldb, const float* bs,
+              const void* bias, void* C, int64_t ldc, int ctype, int64_t M, int64_t N, int64_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

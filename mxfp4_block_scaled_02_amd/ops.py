@@ -27,7 +27,8 @@ EXPORTED = ["mxfp4_status_str", "mxfp4_quant", "mxfp4_rmsnorm_quant", "mxfp4_pac
             "gemm_a4w4_fused_dump_bytes",
             "gemm_a4w4_fused_dump",
             "gemm_a4w4", "grouped_gemm_a4w4_workspace_bytes", "grouped_gemm_a4w4", "grouped_gemm_a4w4_dump_bytes",
-            "grouped_gemm_a4w4_dump_copies", "grouped_gemm_a4w4_dump", "grouped_gemm_a4w4_mnk", "grouped_gemm_nvfp4"]
+            "grouped_gemm_a4w4_dump_copies", "grouped_gemm_a4w4_dump", "grouped_gemm_a4w4_mnk", "grouped_gemm_nvfp4",
+            "int8_quant", "int8_rmsnorm_quant", "gemm_a8w8"]
 
 
 class Mxfp4Error(RuntimeError):
@@ -102,6 +103,11 @@ def lib() -> ctypes.CDLL:
         L.grouped_gemm_a4w4_mnk.argtypes = [ctypes.POINTER(GroupMnk), i32, vp]
         L.grouped_gemm_a4w4_mnk.restype = i32
         L.grouped_gemm_nvfp4.argtypes, L.grouped_gemm_nvfp4.restype = [ctypes.POINTER(GroupNv), i32, vp], i32
+        L.int8_quant.argtypes, L.int8_quant.restype = [vp, i64, i32, vp, i64, vp, i64, i64, vp], i32
+        L.int8_rmsnorm_quant.argtypes = [vp, i64, vp, i64, vp, ctypes.c_float, i32, vp, i64, vp, i64, vp, i64, i64, vp]
+        L.int8_rmsnorm_quant.restype = i32
+        L.gemm_a8w8.argtypes = [vp, i64, vp, vp, i64, vp, vp, vp, i64, i32, i64, i64, i64, vp]
+        L.gemm_a8w8.restype = i32
         _lib = L
         return L
 
@@ -395,3 +401,129 @@ def grouped_gemm_nvfp4(problems, out_list=None):
     arr = (GroupNv * len(descs))(*descs)
     _check(lib().grouped_gemm_nvfp4(arr, len(descs), _stream(problems[0][0])), "grouped_gemm_nvfp4")
     return outs if out_list is None else out_list
+
+
+# The 8-bit integer path. MXFP4_TYPE_* of include/mxfp4.h by torch type.
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device) -> int:
+    """Checks a [rows, cols] argument with unit column stride and returns its row stride (of one row: its length)."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    row, col = t.stride()
+    if col != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return row if shape[0] > 1 else shape[1]
+
+
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> int:
+    """Checks a contiguous [n] argument and returns its address."""
+    if t.device != device or t.dtype != dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on {device}")
+    return t.data_ptr()
+
+
+def _typed(x: torch.Tensor, name: str) -> int:
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if x.dtype not in TYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    return TYPES[x.dtype]
+
+
+def _codes(x: torch.Tensor, out):
+    """The (q, s) outputs of a quantising call on x, their addresses and q's row stride."""
+    M, K = x.shape
+    if out is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+        return q, s, K
+    q, s = out
+    ldq = _matrix(q, "q", torch.int8, (M, K), x.device)
+    _vector(s, "s", torch.float32, M, x.device)
+    return q, s, ldq
+
+
+def _call(fn, where: str, device: torch.device, *args) -> None:
+    """fn(*args, stream) on `device` and its current stream, whatever device is current."""
+    st = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, st), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, st), where)
+
+
+def int8_quant(x: torch.Tensor, out=None):
+    """bf16, fp16 or fp32 [M, K] -> (q int8 [M, K], s float32 [M]), x ~ q * s[:, None]: activations by token,
+    or a weight [N, K] by output channel. `out` = (q, s) reuses given buffers."""
+    dt = _typed(x, "x")
+    M, K = x.shape
+    ldx = _matrix(x, "x", x.dtype, (M, K), x.device)
+    q, s, ldq = _codes(x, out)
+    _call(lib().int8_quant, "int8_quant", x.device, x.data_ptr(), ldx, dt, q.data_ptr(), ldq, s.data_ptr(), M, K)
+    return q, s
+
+
+def int8_rmsnorm_quant(x: torch.Tensor, w: torch.Tensor, eps: float, residual: torch.Tensor | None = None, out=None):
+    """RMSNorm of each row of x [M, K] (bf16, fp16 or fp32) with weight w [K] of the same type, then int8 codes:
+    (q int8 [M, K], s float32 [M]). With a residual [M, K] of the same type the norm is of h = x + residual, and
+    (q, s, h) is returned. `out` = (q, s) or (q, s, h) reuses given buffers; h may be x or residual itself."""
+    dt = _typed(x, "x")
+    M, K = x.shape
+    dev = x.device
+    ldx = _matrix(x, "x", x.dtype, (M, K), dev)
+    wp = _vector(w, "w", x.dtype, K, dev)
+    if residual is None:
+        q, s, ldq = _codes(x, out)
+        _call(lib().int8_rmsnorm_quant, "int8_rmsnorm_quant", dev, x.data_ptr(), ldx, None, 0, wp, float(eps), dt, None,
+              0, q.data_ptr(), ldq, s.data_ptr(), M, K)
+        return q, s
+    ldr = _matrix(residual, "residual", x.dtype, (M, K), dev)
+    if out is None:
+        q, s, ldq = _codes(x, None)
+        h = torch.empty((M, K), dtype=x.dtype, device=dev)
+        ldh = K
+    else:
+        q, s, h = out
+        _, _, ldq = _codes(x, (q, s))
+        ldh = _matrix(h, "h", x.dtype, (M, K), dev)
+    _call(lib().int8_rmsnorm_quant, "int8_rmsnorm_quant", dev, x.data_ptr(), ldx, residual.data_ptr(), ldr, wp,
+          float(eps), dt, h.data_ptr(), ldh, q.data_ptr(), ldq, s.data_ptr(), M, K)
+    return q, s, h
+
+
+def gemm_a8w8(aq: torch.Tensor, a_scale: torch.Tensor, bq: torch.Tensor, b_scale: torch.Tensor,
+              bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """C[M, N] = (aq . bq^T) * a_scale[:, None] * b_scale[None, :] (+ bias): aq int8 [M, K] with a float32 scale per
+    token, bq int8 [N, K] with one per output channel (both from int8_quant, for example), bias [N] of the type of C.
+    C has `out_dtype` (bf16, fp16 or fp32), or is `out` with its own type."""
+    if not aq.is_cuda or aq.dim() != 2 or bq.dim() != 2:
+        raise ValueError("aq and bq must be 2-D CUDA (HIP) tensors")
+    dev = aq.device
+    M, K = aq.shape
+    N = bq.shape[0]
+    lda = _matrix(aq, "aq", torch.int8, (M, K), dev)
+    ldb = _matrix(bq, "bq", torch.int8, (N, K), dev)
+    ap = _vector(a_scale, "a_scale", torch.float32, M, dev)
+    bp = _vector(b_scale, "b_scale", torch.float32, N, dev)
+    if out is None:
+        if out_dtype not in TYPES:
+            raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        ldc = N
+    else:
+        _typed(out, "out")
+        ldc = _matrix(out, "out", out.dtype, (M, N), dev)
+    cp = None if bias is None else _vector(bias, "bias", out.dtype, N, dev)
+    _call(lib().gemm_a8w8, "gemm_a8w8", dev, aq.data_ptr(), lda, ap, bq.data_ptr(), ldb, bp, cp, out.data_ptr(), ldc,
+          TYPES[out.dtype], M, N, K)
+    return out

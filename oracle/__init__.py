@@ -26,3 +26,4 @@ from .mx import (  # noqa: F401
 )
 from . import rmsnorm  # noqa: F401,E402  (RMSNorm followed by MXFP4 quantisation)
 from . import nvfp4  # noqa: F401,E402  (NVFP4: E2M1 with one E4M3 scale per 16)
+from . import int8  # noqa: F401,E402  (int8 row codes, residual RMS norm, scaled integer product)
