@@ -456,6 +456,16 @@ int int8_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t
 int gemm_a8w8(const void* Aq, int64_t lda, const float* as, const void* Bq, int64_t ldb, const float* bs,
               const void* bias, void* C, int64_t ldc, int ctype, int64_t M, int64_t N, int64_t K, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * gemm_a8w8_path -- the kernel that gemm_a8w8 runs for a shape: a pure function of
+ * (M, N, K), computed on the host without a GPU; 1 to MXFP4_A8W8_PATHS in the order
+ * skinny 16x16, 32x16, 32x32 (rows x columns of C per workgroup, K split over its
+ * waves), ring 32x32, 64x32, 64x64, 128x64, 128x128, 128x256, large 256x256; 0 for a
+ * shape the call rejects. Every path gives the same C. For callers and tests.
+ * ------------------------------------------------------------------------- */
+#define MXFP4_A8W8_PATHS 10
+int gemm_a8w8_path(int64_t M, int64_t N, int64_t K);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,7 +28,7 @@ EXPORTED = ["mxfp4_status_str", "mxfp4_quant", "mxfp4_rmsnorm_quant", "mxfp4_pac
             "gemm_a4w4_fused_dump",
             "gemm_a4w4", "grouped_gemm_a4w4_workspace_bytes", "grouped_gemm_a4w4", "grouped_gemm_a4w4_dump_bytes",
             "grouped_gemm_a4w4_dump_copies", "grouped_gemm_a4w4_dump", "grouped_gemm_a4w4_mnk", "grouped_gemm_nvfp4",
-            "int8_quant", "int8_rmsnorm_quant", "gemm_a8w8"]
+            "int8_quant", "int8_rmsnorm_quant", "gemm_a8w8", "gemm_a8w8_path"]
 
 
 class Mxfp4Error(RuntimeError):
@@ -108,6 +108,7 @@ def lib() -> ctypes.CDLL:
         L.int8_rmsnorm_quant.restype = i32
         L.gemm_a8w8.argtypes = [vp, i64, vp, vp, i64, vp, vp, vp, i64, i32, i64, i64, i64, vp]
         L.gemm_a8w8.restype = i32
+        L.gemm_a8w8_path.argtypes, L.gemm_a8w8_path.restype = [i64, i64, i64], i32
         _lib = L
         return L
 
@@ -407,58 +408,67 @@ def grouped_gemm_nvfp4(problems, out_list=None):
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device) -> int:
+A8W8_PATHS = dict(enumerate(["skinny_16x16", "skinny_32x16", "skinny_32x32", "ring_32x32", "ring_64x32", "ring_64x64",
+                             "ring_128x64", "ring_128x128", "ring_128x256", "large_256x256"], 1))
+
+# These calls are short (the kernels of a decode step take a few microseconds), so the binding keeps the host's part
+# short too: the checks read each attribute once, and the raw handle of the current stream spares building a Stream.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int, device: int) -> int:
     """Checks a [rows, cols] argument with unit column stride and returns its row stride (of one row: its length)."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on device {device}, got {t.device}")
     row, col = t.stride()
-    if col != 1:
+    if col != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return row if shape[0] > 1 else shape[1]
+    return row if rows > 1 else cols
 
 
-def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> int:
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> int:
     """Checks a contiguous [n] argument and returns its address."""
-    if t.device != device or t.dtype != dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on {device}")
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on device {device}")
     return t.data_ptr()
 
 
 def _typed(x: torch.Tensor, name: str) -> int:
+    """MXFP4_TYPE_* of a 2-D device tensor."""
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    if x.dtype not in TYPES:
+    dt = TYPES.get(x.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
-    return TYPES[x.dtype]
+    return dt
 
 
-def _codes(x: torch.Tensor, out):
-    """The (q, s) outputs of a quantising call on x, their addresses and q's row stride."""
-    M, K = x.shape
+def _codes(x: torch.Tensor, M: int, K: int, dev: int, out):
+    """The (q, s) outputs of a quantising call on x, and q's row stride."""
     if out is None:
-        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-        s = torch.empty((M,), dtype=torch.float32, device=x.device)
-        return q, s, K
+        device = x.device
+        return torch.empty((M, K), dtype=torch.int8, device=device), torch.empty((M,), dtype=torch.float32, device=device), K
     q, s = out
-    ldq = _matrix(q, "q", torch.int8, (M, K), x.device)
-    _vector(s, "s", torch.float32, M, x.device)
+    ldq = _matrix(q, "q", torch.int8, M, K, dev)
+    _vector(s, "s", torch.float32, M, dev)
     return q, s, ldq
 
 
-def _call(fn, where: str, device: torch.device, *args) -> None:
-    """fn(*args, stream) on `device` and its current stream, whatever device is current."""
-    st = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, st), where)
+def _call(fn, where: str, dev: int, *args) -> None:
+    """fn(*args, stream) on device `dev` and its current stream, whatever device is current."""
+    if dev == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, st), where)
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status:
+        raise Mxfp4Error(status, where)
 
 
 def int8_quant(x: torch.Tensor, out=None):
@@ -466,9 +476,10 @@ def int8_quant(x: torch.Tensor, out=None):
     or a weight [N, K] by output channel. `out` = (q, s) reuses given buffers."""
     dt = _typed(x, "x")
     M, K = x.shape
-    ldx = _matrix(x, "x", x.dtype, (M, K), x.device)
-    q, s, ldq = _codes(x, out)
-    _call(lib().int8_quant, "int8_quant", x.device, x.data_ptr(), ldx, dt, q.data_ptr(), ldq, s.data_ptr(), M, K)
+    dev = x.get_device()
+    ldx = _matrix(x, "x", x.dtype, M, K, dev)
+    q, s, ldq = _codes(x, M, K, dev, out)
+    _call((_lib or lib()).int8_quant, "int8_quant", dev, x.data_ptr(), ldx, dt, q.data_ptr(), ldq, s.data_ptr(), M, K)
     return q, s
 
 
@@ -478,26 +489,27 @@ def int8_rmsnorm_quant(x: torch.Tensor, w: torch.Tensor, eps: float, residual: t
     (q, s, h) is returned. `out` = (q, s) or (q, s, h) reuses given buffers; h may be x or residual itself."""
     dt = _typed(x, "x")
     M, K = x.shape
-    dev = x.device
-    ldx = _matrix(x, "x", x.dtype, (M, K), dev)
+    dev = x.get_device()
+    ldx = _matrix(x, "x", x.dtype, M, K, dev)
     wp = _vector(w, "w", x.dtype, K, dev)
+    h, rp, ldr, hp, ldh = None, None, 0, None, 0
     if residual is None:
-        q, s, ldq = _codes(x, out)
-        _call(lib().int8_rmsnorm_quant, "int8_rmsnorm_quant", dev, x.data_ptr(), ldx, None, 0, wp, float(eps), dt, None,
-              0, q.data_ptr(), ldq, s.data_ptr(), M, K)
-        return q, s
-    ldr = _matrix(residual, "residual", x.dtype, (M, K), dev)
-    if out is None:
-        q, s, ldq = _codes(x, None)
-        h = torch.empty((M, K), dtype=x.dtype, device=dev)
-        ldh = K
+        q, s, ldq = _codes(x, M, K, dev, out)
     else:
-        q, s, h = out
-        _, _, ldq = _codes(x, (q, s))
-        ldh = _matrix(h, "h", x.dtype, (M, K), dev)
-    _call(lib().int8_rmsnorm_quant, "int8_rmsnorm_quant", dev, x.data_ptr(), ldx, residual.data_ptr(), ldr, wp,
-          float(eps), dt, h.data_ptr(), ldh, q.data_ptr(), ldq, s.data_ptr(), M, K)
-    return q, s, h
+        ldr = _matrix(residual, "residual", x.dtype, M, K, dev)
+        rp = residual.data_ptr()
+        if out is None:
+            h = torch.empty((M, K), dtype=x.dtype, device=x.device)
+            q, s, ldq = _codes(x, M, K, dev, None)
+            ldh = K
+        else:
+            q, s, h = out
+            _, _, ldq = _codes(x, M, K, dev, (q, s))
+            ldh = _matrix(h, "h", x.dtype, M, K, dev)
+        hp = h.data_ptr()
+    _call((_lib or lib()).int8_rmsnorm_quant, "int8_rmsnorm_quant", dev, x.data_ptr(), ldx, rp, ldr, wp, float(eps), dt,
+          hp, ldh, q.data_ptr(), ldq, s.data_ptr(), M, K)
+    return (q, s) if residual is None else (q, s, h)
 
 
 def gemm_a8w8(aq: torch.Tensor, a_scale: torch.Tensor, bq: torch.Tensor, b_scale: torch.Tensor,
@@ -508,22 +520,32 @@ def gemm_a8w8(aq: torch.Tensor, a_scale: torch.Tensor, bq: torch.Tensor, b_scale
     C has `out_dtype` (bf16, fp16 or fp32), or is `out` with its own type."""
     if not aq.is_cuda or aq.dim() != 2 or bq.dim() != 2:
         raise ValueError("aq and bq must be 2-D CUDA (HIP) tensors")
-    dev = aq.device
+    dev = aq.get_device()
     M, K = aq.shape
     N = bq.shape[0]
-    lda = _matrix(aq, "aq", torch.int8, (M, K), dev)
-    ldb = _matrix(bq, "bq", torch.int8, (N, K), dev)
+    lda = _matrix(aq, "aq", torch.int8, M, K, dev)
+    ldb = _matrix(bq, "bq", torch.int8, N, K, dev)
     ap = _vector(a_scale, "a_scale", torch.float32, M, dev)
     bp = _vector(b_scale, "b_scale", torch.float32, N, dev)
     if out is None:
-        if out_dtype not in TYPES:
+        ct = TYPES.get(out_dtype)
+        if ct is None:
             raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = torch.empty((M, N), dtype=out_dtype, device=aq.device)
         ldc = N
     else:
-        _typed(out, "out")
-        ldc = _matrix(out, "out", out.dtype, (M, N), dev)
+        ct = _typed(out, "out")
+        ldc = _matrix(out, "out", out.dtype, M, N, dev)
     cp = None if bias is None else _vector(bias, "bias", out.dtype, N, dev)
-    _call(lib().gemm_a8w8, "gemm_a8w8", dev, aq.data_ptr(), lda, ap, bq.data_ptr(), ldb, bp, cp, out.data_ptr(), ldc,
-          TYPES[out.dtype], M, N, K)
+    _call((_lib or lib()).gemm_a8w8, "gemm_a8w8", dev, aq.data_ptr(), lda, ap, bq.data_ptr(), ldb, bp, cp,
+          out.data_ptr(), ldc, ct, M, N, K)
     return out
+
+
+def a8w8_path(M: int, N: int, K: int) -> str:
+    """Name of the kernel gemm_a8w8 runs for (M, N, K), rows x columns of C per workgroup; raises for a shape the
+    call rejects."""
+    p = int(lib().gemm_a8w8_path(M, N, K))
+    if p not in A8W8_PATHS:
+        raise ValueError(f"gemm_a8w8 rejects M={M} N={N} K={K}")
+    return A8W8_PATHS[p]

@@ -12,6 +12,7 @@ import torch
 
 from mxfp4_block_scaled_02_amd import ops
 from oracle import int8 as o8
+from tests.test_int8_abi import PATH_SHAPES
 
 pytestmark = pytest.mark.gpu
 
@@ -209,6 +210,12 @@ SHAPES = [(1, 1, 16), (1, 16, 64), (4, 256, 512), (3, 17, 48), (16, 33, 128), (1
           (1, 100, 8192), (32, 130, 2064), (33, 70, 1040), (48, 257, 528), (64, 64, 256), (65, 129, 272), (100, 31, 4096),
           (127, 255, 400), (128, 256, 1024), (129, 257, 1040), (200, 512, 2048), (255, 300, 96), (256, 256, 128),
           (257, 511, 1936), (300, 1000, 640), (511, 513, 272), (513, 1025, 336), (600, 90, 208)]
+
+
+@pytest.mark.parametrize("path,M,N,K", PATH_SHAPES)
+def test_gemm_paths(path, M, N, K):
+    check_gemm(np.random.default_rng(M + N + K), M, N, K, "fp32", True, (16, 32, 0))
+    check_gemm(np.random.default_rng(M + N + K + 1), M, N, K, "bf16", False, (0, 0, 6), full=True)
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

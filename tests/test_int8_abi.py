@@ -76,27 +76,65 @@ def test_binding_refuses_host_tensors():
         ops.gemm_a8w8(q, s, q, s)
 
 
-@pytest.mark.parametrize("tensor,dtype,shape,what", [
-    (torch.zeros(2, 32, dtype=torch.int8), torch.uint8, (2, 32), "must be"),
-    (torch.zeros(2, 32, dtype=torch.int8), torch.int8, (2, 16), "must be"),
-    (torch.zeros(32, 2, dtype=torch.int8).t(), torch.int8, (2, 32), "unit column stride"),
+@pytest.mark.parametrize("tensor,dtype,shape,device,what", [
+    (torch.zeros(2, 32, dtype=torch.int8), torch.uint8, (2, 32), -1, "must be torch.uint8"),
+    (torch.zeros(2, 32, dtype=torch.int8), torch.int8, (2, 16), -1, "must be"),
+    (torch.zeros(32, dtype=torch.int8), torch.int8, (1, 32), -1, "must be"),
+    (torch.zeros(32, 2, dtype=torch.int8).t(), torch.int8, (2, 32), -1, "unit column stride"),
+    (torch.zeros(2, 32, dtype=torch.int8), torch.int8, (2, 32), 0, "on device 0"),
 ])
-def test_binding_matrix_check(tensor, dtype, shape, what):
+def test_binding_matrix_check(tensor, dtype, shape, device, what):
     with pytest.raises(ValueError, match=what):
-        ops._matrix(tensor, "t", dtype, shape, tensor.device)
+        ops._matrix(tensor, "t", dtype, *shape, device)
 
 
 def test_binding_stride_of_a_single_row_is_its_length():
     one = torch.zeros(8, 64, dtype=torch.int8)[3:4]
-    assert ops._matrix(one, "t", torch.int8, (1, 64), one.device) == 64
+    assert ops._matrix(one, "t", torch.int8, 1, 64, -1) == 64
     odd = torch.zeros(64, dtype=torch.int8).as_strided((1, 64), (1, 1))
-    assert ops._matrix(odd, "t", torch.int8, (1, 64), odd.device) == 64
+    assert ops._matrix(odd, "t", torch.int8, 1, 64, -1) == 64
 
 
 def test_binding_vector_check():
     with pytest.raises(ValueError, match="contiguous"):
-        ops._vector(torch.zeros(8)[::2], "t", torch.float32, 4, torch.device("cpu"))
+        ops._vector(torch.zeros(8)[::2], "t", torch.float32, 4, -1)
     with pytest.raises(ValueError, match="length 5"):
-        ops._vector(torch.zeros(4), "t", torch.float32, 5, torch.device("cpu"))
+        ops._vector(torch.zeros(4), "t", torch.float32, 5, -1)
     with pytest.raises(ValueError, match="float32"):
-        ops._vector(torch.zeros(4, dtype=torch.float64), "t", torch.float32, 4, torch.device("cpu"))
+        ops._vector(torch.zeros(4, dtype=torch.float64), "t", torch.float32, 4, -1)
+
+
+@pytest.mark.parametrize("M,N,K", [(0, 16, 64), (16, 0, 64), (16, 16, 0), (16, 16, 24), (16, 16, 131072),
+                                   ((1 << 24) + 1, 16, 64), (1 << 24, 1 << 24, 64)])
+def test_path_of_a_rejected_shape(M, N, K):
+    assert ops.lib().gemm_a8w8_path(M, N, K) == 0
+    with pytest.raises(ValueError, match="rejects"):
+        ops.a8w8_path(M, N, K)
+
+
+# Each path with row, column and K tails: K of fewer steps than the ring's stages, of many, and tails of 16 to 112 bytes.
+PATH_SHAPES = [("skinny_16x16", 17, 33, 144), ("skinny_16x16", 15, 1001, 7184), ("skinny_32x16", 17, 2050, 528),
+               ("skinny_32x16", 31, 3000, 7120), ("skinny_32x32", 33, 2050, 1040), ("skinny_32x32", 17, 4100, 2096),
+               ("ring_32x32", 17, 33, 16), ("ring_32x32", 33, 257, 16), ("ring_32x32", 33, 2051, 784),
+               ("ring_64x32", 257, 1030, 16), ("ring_64x32", 97, 2113, 1040), ("ring_64x64", 257, 2050, 16),
+               ("ring_64x64", 65, 4099, 2064), ("ring_128x64", 515, 2050, 16), ("ring_128x64", 257, 4100, 144),
+               ("ring_128x64", 390, 3001, 1040), ("ring_128x128", 1030, 2050, 16), ("ring_128x128", 515, 4100, 144),
+               ("ring_128x128", 1030, 2051, 1040), ("ring_128x256", 1030, 4100, 16), ("ring_128x256", 1300, 4100, 528),
+               ("large_256x256", 2067, 3985, 272), ("large_256x256", 2586, 3141, 1040)]
+
+
+@pytest.mark.parametrize("path,M,N,K", PATH_SHAPES)
+def test_path_shapes(path, M, N, K):
+    assert ops.a8w8_path(M, N, K) == path
+
+
+def test_paths_follow_the_measured_order():
+    """Few tokens take the small tiles, prefills the large ones, and every path is some shape's."""
+    assert ops.a8w8_path(1, 4096, 7168) == "skinny_16x16"
+    assert ops.a8w8_path(16, 2112, 7168) == "skinny_16x16"
+    assert ops.a8w8_path(4096, 4096, 7168) == "large_256x256"
+    assert ops.a8w8_path(1024, 4096, 7168) == "ring_128x128"
+    seen = {ops.a8w8_path(M, N, K) for M in (1, 16, 32, 64, 128, 256, 512, 1024, 2048, 4096)
+            for N in (256, 1024, 2112, 4096, 7168) for K in (512, 2048, 7168)}
+    assert seen == set(ops.A8W8_PATHS.values())
+    assert ops.a8w8_path(1 << 24, 1024, 131056) in ops.A8W8_PATHS.values()
