@@ -412,8 +412,10 @@ A8W8_PATHS = dict(enumerate(["skinny_16x16", "skinny_32x16", "skinny_32x32", "ri
                              "ring_128x64", "ring_128x128", "ring_128x256", "large_256x256"], 1))
 
 # These calls are short (the kernels of a decode step take a few microseconds), so the binding keeps the host's part
-# short too: the checks read each attribute once, and the raw handle of the current stream spares building a Stream.
+# short too: the raw handle of the current stream spares building a Stream, the checks read an attribute once, and a
+# check's message is put together only when it fails.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int, device: int) -> int:
@@ -424,6 +426,8 @@ def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on device {device}, got {t.device}")
+    if t.is_contiguous():
+        return cols
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
@@ -432,7 +436,7 @@ def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int
 
 def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> int:
     """Checks a contiguous [n] argument and returns its address."""
-    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on device {device}")
     return t.data_ptr()
 
@@ -453,7 +457,7 @@ def _codes(x: torch.Tensor, M: int, K: int, dev: int, out):
     """The (q, s) outputs of a quantising call on x, and q's row stride."""
     if out is None:
         device = x.device
-        return torch.empty((M, K), dtype=torch.int8, device=device), torch.empty((M,), dtype=torch.float32, device=device), K
+        return torch.empty(M, K, dtype=torch.int8, device=device), torch.empty(M, dtype=torch.float32, device=device), K
     q, s = out
     ldq = _matrix(q, "q", torch.int8, M, K, dev)
     _vector(s, "s", torch.float32, M, dev)
@@ -462,7 +466,7 @@ def _codes(x: torch.Tensor, M: int, K: int, dev: int, out):
 
 def _call(fn, where: str, dev: int, *args) -> None:
     """fn(*args, stream) on device `dev` and its current stream, whatever device is current."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -499,7 +503,7 @@ def int8_rmsnorm_quant(x: torch.Tensor, w: torch.Tensor, eps: float, residual: t
         ldr = _matrix(residual, "residual", x.dtype, M, K, dev)
         rp = residual.data_ptr()
         if out is None:
-            h = torch.empty((M, K), dtype=x.dtype, device=x.device)
+            h = torch.empty(M, K, dtype=x.dtype, device=x.device)
             q, s, ldq = _codes(x, M, K, dev, None)
             ldh = K
         else:
@@ -531,7 +535,7 @@ def gemm_a8w8(aq: torch.Tensor, a_scale: torch.Tensor, bq: torch.Tensor, b_scale
         ct = TYPES.get(out_dtype)
         if ct is None:
             raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-        out = torch.empty((M, N), dtype=out_dtype, device=aq.device)
+        out = torch.empty(M, N, dtype=out_dtype, device=aq.device)
         ldc = N
     else:
         ct = _typed(out, "out")

@@ -56,9 +56,9 @@ def codes_buffers(M, K, pad):
     return q, s
 
 
-# Every row kernel: pieces of 16 bytes up to 64, 256, 512, 1024, 4096 and past, on both sides of each limit.
-ROWS = [(1, 16), (3, 48), (5, 512), (4, 528), (7, 1040), (2, 2048), (3, 2064), (2, 4096), (3, 4112), (9, 7168),
-        (2, 8192), (3, 8208), (2, 16400), (1, 32768), (2, 32784), (1, 100000)]
+# Every row kernel: pieces of 16 bytes up to 64, 128, 256, 512, 1024, 2048, 4096 and past, on both sides of each limit.
+ROWS = [(1, 16), (3, 48), (6, 256), (5, 512), (4, 528), (2, 1024), (7, 1040), (2, 2048), (3, 2064), (2, 4096), (3, 4112),
+        (9, 7168), (2, 8192), (3, 8208), (1, 16384), (2, 16400), (1, 32768), (2, 32784), (1, 100000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
