@@ -420,25 +420,21 @@ _current_device = torch._C._cuda_getDevice
 
 def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int, device: int) -> int:
     """Checks a [rows, cols] argument with unit column stride and returns its row stride (of one row: its length)."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on device {device}, got {t.device}")
-    if t.is_contiguous():
-        return cols
-    row, col = t.stride()
-    if col != 1 and cols > 1:
+    if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols):
+        if t.is_contiguous():
+            return cols
+        row, col = t.stride()
+        if col == 1 or cols == 1:
+            return row if rows > 1 else cols
         raise ValueError(f"{name} must have unit column stride")
-    return row if rows > 1 else cols
+    raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on device {device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> int:
     """Checks a contiguous [n] argument and returns its address."""
-    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on device {device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == device and t.dim() == 1 and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on device {device}")
 
 
 def _typed(x: torch.Tensor, name: str) -> int:
@@ -464,13 +460,13 @@ def _codes(x: torch.Tensor, M: int, K: int, dev: int, out):
     return q, s, ldq
 
 
-def _call(fn, where: str, dev: int, *args) -> None:
-    """fn(*args, stream) on device `dev` and its current stream, whatever device is current."""
+def _call(fn, where: str, dev: int, args) -> None:
+    """fn(*args) with device `dev` current, whatever device is."""
     if dev == _current_device():
-        status = fn(*args, _raw_stream(dev))
+        status = fn(*args)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev))
+            status = fn(*args)
     if status:
         raise Mxfp4Error(status, where)
 
@@ -483,7 +479,8 @@ def int8_quant(x: torch.Tensor, out=None):
     dev = x.get_device()
     ldx = _matrix(x, "x", x.dtype, M, K, dev)
     q, s, ldq = _codes(x, M, K, dev, out)
-    _call((_lib or lib()).int8_quant, "int8_quant", dev, x.data_ptr(), ldx, dt, q.data_ptr(), ldq, s.data_ptr(), M, K)
+    _call((_lib or lib()).int8_quant, "int8_quant", dev,
+          (x.data_ptr(), ldx, dt, q.data_ptr(), ldq, s.data_ptr(), M, K, _raw_stream(dev)))
     return q, s
 
 
@@ -511,8 +508,8 @@ def int8_rmsnorm_quant(x: torch.Tensor, w: torch.Tensor, eps: float, residual: t
             _, _, ldq = _codes(x, M, K, dev, (q, s))
             ldh = _matrix(h, "h", x.dtype, M, K, dev)
         hp = h.data_ptr()
-    _call((_lib or lib()).int8_rmsnorm_quant, "int8_rmsnorm_quant", dev, x.data_ptr(), ldx, rp, ldr, wp, float(eps), dt,
-          hp, ldh, q.data_ptr(), ldq, s.data_ptr(), M, K)
+    _call((_lib or lib()).int8_rmsnorm_quant, "int8_rmsnorm_quant", dev,
+          (x.data_ptr(), ldx, rp, ldr, wp, eps, dt, hp, ldh, q.data_ptr(), ldq, s.data_ptr(), M, K, _raw_stream(dev)))
     return (q, s) if residual is None else (q, s, h)
 
 
@@ -541,8 +538,8 @@ def gemm_a8w8(aq: torch.Tensor, a_scale: torch.Tensor, bq: torch.Tensor, b_scale
         ct = _typed(out, "out")
         ldc = _matrix(out, "out", out.dtype, M, N, dev)
     cp = None if bias is None else _vector(bias, "bias", out.dtype, N, dev)
-    _call((_lib or lib()).gemm_a8w8, "gemm_a8w8", dev, aq.data_ptr(), lda, ap, bq.data_ptr(), ldb, bp, cp,
-          out.data_ptr(), ldc, ct, M, N, K)
+    _call((_lib or lib()).gemm_a8w8, "gemm_a8w8", dev,
+          (aq.data_ptr(), lda, ap, bq.data_ptr(), ldb, bp, cp, out.data_ptr(), ldc, ct, M, N, K, _raw_stream(dev)))
     return out
 
 

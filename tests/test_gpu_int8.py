@@ -408,5 +408,5 @@ def test_binding_refusals_on_the_device():
         ops.gemm_a8w8(q, s, q, s, out_dtype=torch.int32)
     with pytest.raises(ValueError, match="out must be"):
         ops.gemm_a8w8(q, s, q, s, out=x[:, :3])
-    with pytest.raises(ValueError, match="must be on"):
+    with pytest.raises(ValueError, match="on device 0"):
         ops.gemm_a8w8(q, s, q.cpu(), s)
