@@ -24,6 +24,24 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
+// Several elements of C at any element's address (rows need not be aligned to more):
+// the hardware takes such stores, one instruction each.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
+template <int CT>
+struct Packed {
+  static constexpr int kSize = CT == MXFP4_TYPE_F32 ? 4 : 2;
+  static __device__ __forceinline__ void store16(void* at, const u32x4& v) {
+    if constexpr (kSize == 4)
+      *reinterpret_cast<u32x4_at4*>(at) = v;
+    else
+      *reinterpret_cast<u32x4_at2*>(at) = v;
+  }
+};
+
 struct GemmArgs {
   const uint8_t* A;
   int64_t lda;
@@ -68,16 +86,15 @@ __device__ __forceinline__ void store_one(const GemmArgs& p, int64_t m, int n, f
 __device__ __forceinline__ int unit_piece(int l, int unit_parity) { return 16 * ((l & 7) ^ (l >> 4)) ^ (64 * unit_parity); }
 __device__ __forceinline__ int frag_at(int l, int kk) { return (l & 15) * 128 + 16 * ((4 * kk + (l >> 4)) ^ ((l >> 1) & 7)); }
 
-typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
 // The buffer resource of `window` as scalar words, for the loads written in assembly.
-__device__ __forceinline__ u32x4s window_words(const uint8_t* base, int64_t rows, int64_t ld, int K) {
-  return u32x4s{(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), (uint32_t)((rows - 1) * ld + K), 0x00020000u};
+__device__ __forceinline__ u32x4 window_words(const uint8_t* base, int64_t rows, int64_t ld, int K) {
+  return u32x4{(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), (uint32_t)((rows - 1) * ld + K), 0x00020000u};
 }
 // 1 KB from memory to LDS (16 bytes a lane; lanes out of range write zeros). In
 // assembly: for the intrinsic the compiler waits before every LDS read that follows,
 // which would drain the ring. The kernels wait themselves (wait_loads, and a barrier
 // where other waves read). No register but m0 is written, which nothing else here uses.
-__device__ __forceinline__ void load_to_lds(uint32_t at, int voff, const u32x4s& r) {
+__device__ __forceinline__ void load_to_lds(uint32_t at, int voff, const u32x4& r) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(r) : "memory");
 }
 template <int N>
@@ -130,12 +147,12 @@ struct TileScales {
 // go through the wave's own LDS block (kPitch bytes a row) and out in pieces of 16 bytes.
 template <int CT, int NI>
 struct Strip {
-  static constexpr int kSize = CT == MXFP4_TYPE_F32 ? 4 : 2;
+  static constexpr int kSize = Packed<CT>::kSize;
   static constexpr int kPitch = 16 * NI * kSize + 16;
   static constexpr int kBytes = 16 * kPitch;
   static __device__ __forceinline__ void store(const GemmArgs& p, uint8_t* epi, const v4i (&acc)[NI], float as,
                                                const float4 (&bs)[NI], const float4 (&bias)[NI], int m0, int n0,
-                                               bool wide, int l) {
+                                               int l) {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const float sc[4] = {bs[j].x, bs[j].y, bs[j].z, bs[j].w}, bi[4] = {bias[j].x, bias[j].y, bias[j].z, bias[j].w};
@@ -158,15 +175,15 @@ struct Strip {
     const uint8_t* const from = epi;
     uint8_t* const to = (uint8_t*)p.C + ((int64_t)m0 * p.ldc + n0) * kSize;
     const int rows = min(16, p.M - m0), cols = min(16 * NI, p.N - n0);  // either may be below 1
-    if (wide && cols == 16 * NI) {
+    if (cols >= 16 * NI) {
       constexpr int kPieces = NI * kSize;  // of 16 bytes, in a row
 #pragma unroll
       for (int i = 0; i < 16 * kPieces; i += 64) {
         const int r = (i + l) / kPieces, c = (i + l) % kPieces * 16;
         if (r < rows)
-          *reinterpret_cast<uint4*>(to + r * p.ldc * kSize + c) = *reinterpret_cast<const uint4*>(from + r * kPitch + c);
+          Packed<CT>::store16(to + r * p.ldc * kSize + c, *reinterpret_cast<const u32x4*>(from + r * kPitch + c));
       }
-    } else {  // element by element, neighbouring lanes on neighbouring columns
+    } else {  // the last columns element by element, neighbouring lanes on neighbouring columns
 #pragma unroll 4
       for (int i = l; i < 256 * NI; i += 64) {
         const int r = i / (16 * NI), c = i % (16 * NI);
@@ -181,27 +198,25 @@ struct Strip {
     __builtin_amdgcn_wave_barrier();
   }
 };
-// Four neighbouring elements of C, of which the first `left` exist; `wide`: they may go out as one store.
+// Four neighbouring elements of C, of which the first `left` exist.
 template <int CT>
-__device__ __forceinline__ void store_four(const GemmArgs& p, int64_t m, int n, const float (&v)[4], int left, bool wide) {
-  if (!wide || left < 4) {
+__device__ __forceinline__ void store_four(const GemmArgs& p, int64_t m, int n, const float (&v)[4], int left) {
+  if (left < 4) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (e < left) store_one<CT>(p, m, n + e, v[e]);
     return;
   }
-  uint8_t* const t = (uint8_t*)p.C + (m * p.ldc + n) * Strip<CT, 1>::kSize;
-  if constexpr (CT == MXFP4_TYPE_F32)
-    *reinterpret_cast<float4*>(t) = make_float4(v[0], v[1], v[2], v[3]);
-  else if constexpr (CT == MXFP4_TYPE_BF16)
-    *reinterpret_cast<uint2*>(t) = make_uint2(mx::pack_bf16x2(v[0], v[1]), mx::pack_bf16x2(v[2], v[3]));
-  else
-    *reinterpret_cast<f16x4*>(t) = f16x4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-}
-// Whether C takes 16-byte stores.
-template <int CT>
-__device__ __forceinline__ bool wide_stores(const GemmArgs& p) {
-  return ((uintptr_t)p.C | (uintptr_t)(p.ldc * Strip<CT, 1>::kSize)) % 16 == 0;
+  uint8_t* const t = (uint8_t*)p.C + (m * p.ldc + n) * Packed<CT>::kSize;
+  if constexpr (CT == MXFP4_TYPE_F32) {
+    Packed<CT>::store16(t, u32x4{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
+                                 __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])});
+  } else if constexpr (CT == MXFP4_TYPE_BF16) {
+    *reinterpret_cast<u32x2_at2*>(t) = u32x2{mx::pack_bf16x2(v[0], v[1]), mx::pack_bf16x2(v[2], v[3])};
+  } else {
+    const f16x4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    *reinterpret_cast<u32x2_at2*>(t) = __builtin_bit_cast(u32x2, h);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -222,8 +237,8 @@ __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt)
   const int m0 = (int)(blockIdx.x % (unsigned)mt) * MS, n0 = (int)(blockIdx.x / (unsigned)mt) * NC;
   const int rows = min(MS, p.M - m0), cols = min(NC, p.N - n0);
   const int lda = (int)p.lda, ldb = (int)p.ldb;
-  const u32x4s ar = window_words(p.A + (int64_t)m0 * lda, rows, lda, p.K);
-  const u32x4s br = window_words(p.B + (int64_t)n0 * ldb, cols, ldb, p.K);
+  const u32x4 ar = window_words(p.A + (int64_t)m0 * lda, rows, lda, p.K);
+  const u32x4 br = window_words(p.B + (int64_t)n0 * ldb, cols, ldb, p.K);
   uint8_t* const own = lds + wave * kRing;
   const uint32_t own0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + wave * kRing;
   const int steps = (p.K + 127) / 128;
@@ -287,7 +302,6 @@ __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt)
 #pragma unroll
     for (int i = 0; i < MT; ++i) *reinterpret_cast<v4i*>(own + ((j * MT + i) * 64 + l) * 16) = acc[i][j];
   __syncthreads();
-  const bool wide = ((uintptr_t)p.C | (uintptr_t)(p.ldc * Strip<CT, 1>::kSize)) % (4 * Strip<CT, 1>::kSize) == 0;
 #pragma unroll
   for (int c = 0; c < kRounds; ++c) {
     const int t = (int)threadIdx.x + T * c, m = 16 * ((t >> 6) % MT) + (t & 15), n = 16 * ((t >> 6) / MT) + 4 * (t >> 4 & 3);
@@ -301,7 +315,7 @@ __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt)
       v[e] = (float)sum[e] * as[c] * bs[c][e];
       if (p.bias) v[e] = v[e] + bias[c][e];
     }
-    store_four<CT>(p, m0 + m, n0 + n, v, cols - n, wide);
+    store_four<CT>(p, m0 + m, n0 + n, v, cols - n);
   }
 }
 
@@ -333,8 +347,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_ring_kernel(GemmArgs p, int
   const TileAt tile = tile_at(blockIdx.x, mt, nt);
   const int m0 = tile.m * BM, n0 = tile.n * BN, rows = min(BM, p.M - m0), cols = min(BN, p.N - n0);
   const int lda = (int)p.lda, ldb = (int)p.ldb;
-  const u32x4s ar = window_words(p.A + (int64_t)m0 * lda, rows, lda, p.K);
-  const u32x4s br = window_words(p.B + (int64_t)n0 * ldb, cols, ldb, p.K);
+  const u32x4 ar = window_words(p.A + (int64_t)m0 * lda, rows, lda, p.K);
+  const u32x4 br = window_words(p.B + (int64_t)n0 * ldb, cols, ldb, p.K);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const int avo = (8 * wave * LA + (l >> 3)) * lda, bvo = (8 * wave * LB + (l >> 3)) * ldb;
   auto load = [&](int s, int slot) {  // past K (and in steps past the last) zeros
@@ -407,11 +421,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_ring_kernel(GemmArgs p, int
     bs[j] = *reinterpret_cast<const float4*>(at);
     bias[j] = *reinterpret_cast<const float4*>(at + BM + BN);
   }
-  const bool wide = wide_stores<CT>(p);
 #pragma unroll
   for (int i = 0; i < MI; ++i)
     St::store(p, lds + wave * St::kBytes, acc[i], scales[BN + wm * TM + 16 * i + (l & 15)], bs, bias,
-              m0 + wm * TM + 16 * i, n0 + wn * TN, wide, l);
+              m0 + wm * TM + 16 * i, n0 + wn * TN, l);
 }
 
 // ---------------------------------------------------------------------------
@@ -439,8 +452,8 @@ __global__ __launch_bounds__(512) void gemm_large_kernel(GemmArgs p, int mt, int
   const TileAt tile = tile_at(blockIdx.x, mt, nt);
   const int m0 = tile.m * BM, n0 = tile.n * BN, rows = min(BM, p.M - m0), cols = min(BN, p.N - n0);
   const int lda = (int)p.lda, ldb = (int)p.ldb;
-  const u32x4s ar = window_words(p.A + (int64_t)m0 * lda, rows, lda, p.K);
-  const u32x4s br = window_words(p.B + (int64_t)n0 * ldb, cols, ldb, p.K);
+  const u32x4 ar = window_words(p.A + (int64_t)m0 * lda, rows, lda, p.K);
+  const u32x4 br = window_words(p.B + (int64_t)n0 * ldb, cols, ldb, p.K);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const int avo = (16 * wave + (l >> 3)) * lda, bvo = (16 * wave + (l >> 3)) * ldb;
   // half i of this wave's 16 rows of unit q of step s; past K (and in steps past the last) zeros
@@ -534,11 +547,10 @@ __global__ __launch_bounds__(512) void gemm_large_kernel(GemmArgs p, int mt, int
     bs[j] = *reinterpret_cast<const float4*>(from);
     bias[j] = *reinterpret_cast<const float4*>(from + BM + BN);
   }
-  const bool wide = wide_stores<CT>(p);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int m = 128 * (i >> 2) + wm * 64 + 16 * (i & 3);
-    St::store(p, lds + wave * St::kBytes, acc[i], scales[BN + m + (l & 15)], bs, bias, m0 + m, n0 + wn * 64, wide, l);
+    St::store(p, lds + wave * St::kBytes, acc[i], scales[BN + m + (l & 15)], bs, bias, m0 + m, n0 + wn * 64, l);
   }
 }
 

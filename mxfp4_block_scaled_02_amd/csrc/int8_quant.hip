@@ -42,6 +42,13 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+// Workgroups go kGridX to a row of the grid: one dimension of a launch holds fewer than
+// 2^32 threads, which eight million rows of 512 would pass.
+constexpr int64_t kGridX = (int64_t)1 << 20;
+inline dim3 row_grid(int64_t groups) {
+  return dim3((unsigned)(groups < kGridX ? groups : kGridX), (unsigned)mxh::cdiv(groups, kGridX));
+}
+
 enum Mode { kQuant, kNorm, kNormResidual };
 
 // 16 bytes of a row as fp32 values, and back (round to nearest even).
@@ -184,8 +191,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void row_kernel(RowArgs a) {
   __shared__ double part_sum[W];
   __shared__ uint32_t part_max[W];
   const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  if (W == 1 && row >= a.M) return;  // whole waves, and no barrier with W == 1
+  const int64_t group = (int64_t)blockIdx.y * kGridX + blockIdx.x;
+  const int64_t row = W == 1 ? group * 4 + (threadIdx.x >> 6) : group;
+  if (row >= a.M) return;  // whole workgroups; with W == 1 whole waves, and then there is no barrier
   const int bytes = a.K * P::kSize;
   const __amdgpu_buffer_rsrc_t xr = row_rsrc(a.x + row * a.ldx, bytes);
   u32x4 v[R], w[R];
@@ -269,7 +277,8 @@ __global__ __launch_bounds__(64 * kLongWaves) void row_long_kernel(RowArgs a) {
   constexpr int E = P::kElems, T = 64 * kLongWaves;
   __shared__ double part_sum[kLongWaves];
   __shared__ uint32_t part_max[kLongWaves];
-  const int64_t row = blockIdx.x;
+  const int64_t row = (int64_t)blockIdx.y * kGridX + blockIdx.x;
+  if (row >= a.M) return;
   const int pieces = a.K / E;
   const uint8_t* src = a.x + row * a.ldx;
   float inv = 1.0f;
@@ -321,9 +330,8 @@ __global__ __launch_bounds__(64 * kLongWaves) void row_long_kernel(RowArgs a) {
 template <int DT, int MODE, int W, int R>
 hipError_t launch_row(RowArgs& a, hipStream_t st) {
   void* args[] = {&a};
-  const int64_t grid = W == 1 ? mxh::cdiv(a.M, 4) : a.M;
-  return hipLaunchKernel((const void*)row_kernel<DT, MODE, W, R>, dim3((unsigned)grid), dim3(W == 1 ? 256 : 64 * W),
-                         args, 0, st);
+  return hipLaunchKernel((const void*)row_kernel<DT, MODE, W, R>, row_grid(W == 1 ? mxh::cdiv(a.M, 4) : a.M),
+                         dim3(W == 1 ? 256 : 64 * W), args, 0, st);
 }
 
 // Waves to a row and pieces to a thread: the fewest waves that leave a thread one or two
@@ -343,8 +351,7 @@ hipError_t launch_mode(RowArgs& a, hipStream_t st) {
   if (pieces <= 2048) return launch_row<DT, MODE, 8, 4>(a, st);
   if (pieces <= 4096) return launch_row<DT, MODE, 16, 4>(a, st);
   void* args[] = {&a};
-  return hipLaunchKernel((const void*)row_long_kernel<DT, MODE>, dim3((unsigned)a.M), dim3(64 * kLongWaves), args, 0,
-                         st);
+  return hipLaunchKernel((const void*)row_long_kernel<DT, MODE>, row_grid(a.M), dim3(64 * kLongWaves), args, 0, st);
 }
 
 template <int MODE>

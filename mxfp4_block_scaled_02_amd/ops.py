@@ -509,7 +509,7 @@ def int8_rmsnorm_quant(x: torch.Tensor, w: torch.Tensor, eps: float, residual: t
             ldh = _matrix(h, "h", x.dtype, M, K, dev)
         hp = h.data_ptr()
     _call((_lib or lib()).int8_rmsnorm_quant, "int8_rmsnorm_quant", dev,
-          (x.data_ptr(), ldx, rp, ldr, wp, eps, dt, hp, ldh, q.data_ptr(), ldq, s.data_ptr(), M, K, _raw_stream(dev)))
+          (x.data_ptr(), ldx, rp, ldr, wp, float(eps), dt, hp, ldh, q.data_ptr(), ldq, s.data_ptr(), M, K, _raw_stream(dev)))
     return (q, s) if residual is None else (q, s, h)
 
 

@@ -86,6 +86,22 @@ def test_quant_many_rows(M):
     same(q.cpu().numpy(), qr, "codes")
 
 
+@pytest.mark.parametrize("M,K", [((1 << 20) + 3, 528), ((1 << 22) + 5, 16)])
+def test_quant_more_rows_than_one_row_of_the_grid(M, K):
+    """The rows around the limits (2^20 workgroups of one row, or of four) against the oracle, the others against
+    themselves: the input repeats every 1021 rows."""
+    v = values(np.random.default_rng(M), 1021, K, "bf16")
+    x = dev(v, "bf16").repeat(M // 1021 + 1, 1)[:M]
+    q, s = ops.int8_quant(x)
+    qr, sr = o8.row_codes(v)
+    rows = [0, 1, 1020, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, M - 2, M - 1]
+    at = np.array(rows) % 1021
+    same(s[rows].cpu().numpy(), sr[at], "scales")
+    same(q[rows].cpu().numpy(), qr[at], "codes")
+    n = M // 1021 * 1021
+    assert (q[:n].view(-1, 1021, K) == q[:1021]).all() and (s[:n].view(-1, 1021) == s[:1021]).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("K", [64, 2064, 33024])
 def test_quant_rows_at_the_edges(K, dtype):
