@@ -25,7 +25,8 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 // Several elements of C at any element's address (rows need not be aligned to more):
-// the hardware takes such stores, one instruction each.
+// the hardware takes such stores, one instruction each. Non-temporal: C passes through
+// once, and the operands keep their place in L2 (M2048 N7168 K2048: 28.8 -> 28.0 us).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
@@ -36,9 +37,9 @@ struct Packed {
   static constexpr int kSize = CT == MXFP4_TYPE_F32 ? 4 : 2;
   static __device__ __forceinline__ void store16(void* at, const u32x4& v) {
     if constexpr (kSize == 4)
-      *reinterpret_cast<u32x4_at4*>(at) = v;
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_at4*>(at));
     else
-      *reinterpret_cast<u32x4_at2*>(at) = v;
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_at2*>(at));
   }
 };
 
@@ -143,8 +144,10 @@ struct TileScales {
 };
 
 // 16 rows of a wave's part of C. acc[j] lane l register r is row l%16, column
-// 16*j + 4*(l/16) + r of it (B is the matrix instruction's first operand). The rows
-// go through the wave's own LDS block (kPitch bytes a row) and out in pieces of 16 bytes.
+// 16*j + 4*(l/16) + r of it (B is the matrix instruction's first operand). The rows go
+// through the wave's own LDS block (kPitch bytes a row) and out in pieces of 16 bytes.
+// Strip by strip: the stores of one drain while the next is converted (eight strips
+// put first and stored after: M4096 N4096 K128 10.0 -> 10.9 us).
 template <int CT, int NI>
 struct Strip {
   static constexpr int kSize = Packed<CT>::kSize;
