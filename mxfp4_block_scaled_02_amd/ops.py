@@ -411,52 +411,53 @@ TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 A8W8_PATHS = dict(enumerate(["skinny_16x16", "skinny_32x16", "skinny_32x32", "ring_32x32", "ring_64x32", "ring_64x64",
                              "ring_128x64", "ring_128x128", "ring_128x256", "large_256x256"], 1))
 
-# These calls are short (the kernels of a decode step take a few microseconds), so the binding keeps the host's part
-# short too: the raw handle of the current stream spares building a Stream, the checks read an attribute once, and a
-# check's message is put together only when it fails.
+# These calls are short (the kernels of a decode step take a few microseconds, a launch 2.8), so the host's part is
+# kept short too: the raw handle of the current stream spares building a Stream, and one chain of tests passes the
+# ordinary call (everything contiguous); what fails it goes through the checks below, which either say what is wrong
+# or find the strides.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_I8, _F32 = torch.int8, torch.float32
 
 
 def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int, device: int) -> int:
     """Checks a [rows, cols] argument with unit column stride and returns its row stride (of one row: its length)."""
-    if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols):
-        if t.is_contiguous():
-            return cols
-        row, col = t.stride()
-        if col == 1 or cols == 1:
-            return row if rows > 1 else cols
+    if t.dtype is not dtype or t.get_device() != device or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on device {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    row, col = t.stride()
+    if col != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on device {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    return row if rows > 1 else cols
 
 
-def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> int:
-    """Checks a contiguous [n] argument and returns its address."""
-    if t.dtype is dtype and t.get_device() == device and t.dim() == 1 and t.numel() == n and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on device {device}")
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> None:
+    """Checks a contiguous [n] argument."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on device {device}")
 
 
-def _typed(x: torch.Tensor, name: str) -> int:
-    """MXFP4_TYPE_* of a 2-D device tensor."""
-    if not x.is_cuda:
+def _typed(x: torch.Tensor, name: str):
+    """(MXFP4_TYPE_*, device index, rows, columns) of a 2-D device tensor."""
+    dev, dt = x.get_device(), TYPES.get(x.dtype)
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    dt = TYPES.get(x.dtype)
     if dt is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
-    return dt
+    M, K = x.shape
+    return dt, dev, M, K
 
 
 def _codes(x: torch.Tensor, M: int, K: int, dev: int, out):
     """The (q, s) outputs of a quantising call on x, and q's row stride."""
     if out is None:
         device = x.device
-        return torch.empty(M, K, dtype=torch.int8, device=device), torch.empty(M, dtype=torch.float32, device=device), K
+        return torch.empty(M, K, dtype=_I8, device=device), torch.empty(M, dtype=_F32, device=device), K
     q, s = out
-    ldq = _matrix(q, "q", torch.int8, M, K, dev)
-    _vector(s, "s", torch.float32, M, dev)
+    ldq = _matrix(q, "q", _I8, M, K, dev)
+    _vector(s, "s", _F32, M, dev)
     return q, s, ldq
 
 
@@ -474,10 +475,8 @@ def _call(fn, where: str, dev: int, args) -> None:
 def int8_quant(x: torch.Tensor, out=None):
     """bf16, fp16 or fp32 [M, K] -> (q int8 [M, K], s float32 [M]), x ~ q * s[:, None]: activations by token,
     or a weight [N, K] by output channel. `out` = (q, s) reuses given buffers."""
-    dt = _typed(x, "x")
-    M, K = x.shape
-    dev = x.get_device()
-    ldx = _matrix(x, "x", x.dtype, M, K, dev)
+    dt, dev, M, K = _typed(x, "x")
+    ldx = K if x.is_contiguous() else _matrix(x, "x", x.dtype, M, K, dev)
     q, s, ldq = _codes(x, M, K, dev, out)
     _call((_lib or lib()).int8_quant, "int8_quant", dev,
           (x.data_ptr(), ldx, dt, q.data_ptr(), ldq, s.data_ptr(), M, K, _raw_stream(dev)))
@@ -488,28 +487,33 @@ def int8_rmsnorm_quant(x: torch.Tensor, w: torch.Tensor, eps: float, residual: t
     """RMSNorm of each row of x [M, K] (bf16, fp16 or fp32) with weight w [K] of the same type, then int8 codes:
     (q int8 [M, K], s float32 [M]). With a residual [M, K] of the same type the norm is of h = x + residual, and
     (q, s, h) is returned. `out` = (q, s) or (q, s, h) reuses given buffers; h may be x or residual itself."""
-    dt = _typed(x, "x")
-    M, K = x.shape
-    dev = x.get_device()
-    ldx = _matrix(x, "x", x.dtype, M, K, dev)
-    wp = _vector(w, "w", x.dtype, K, dev)
+    dt, dev, M, K = _typed(x, "x")
+    T = x.dtype
+    ldx = K if x.is_contiguous() else _matrix(x, "x", T, M, K, dev)
+    if not (w.dtype is T and w.get_device() == dev and w.shape == (K,) and w.is_contiguous()):
+        _vector(w, "w", T, K, dev)
     h, rp, ldr, hp, ldh = None, None, 0, None, 0
     if residual is None:
         q, s, ldq = _codes(x, M, K, dev, out)
     else:
-        ldr = _matrix(residual, "residual", x.dtype, M, K, dev)
+        if (residual.dtype is T and residual.get_device() == dev and residual.shape == (M, K)
+                and residual.is_contiguous()):
+            ldr = K
+        else:
+            ldr = _matrix(residual, "residual", T, M, K, dev)
         rp = residual.data_ptr()
         if out is None:
-            h = torch.empty(M, K, dtype=x.dtype, device=x.device)
+            h = torch.empty(M, K, dtype=T, device=x.device)
             q, s, ldq = _codes(x, M, K, dev, None)
             ldh = K
         else:
             q, s, h = out
             _, _, ldq = _codes(x, M, K, dev, (q, s))
-            ldh = _matrix(h, "h", x.dtype, M, K, dev)
+            ldh = _matrix(h, "h", T, M, K, dev)
         hp = h.data_ptr()
     _call((_lib or lib()).int8_rmsnorm_quant, "int8_rmsnorm_quant", dev,
-          (x.data_ptr(), ldx, rp, ldr, wp, float(eps), dt, hp, ldh, q.data_ptr(), ldq, s.data_ptr(), M, K, _raw_stream(dev)))
+          (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), float(eps), dt, hp, ldh, q.data_ptr(), ldq, s.data_ptr(), M, K,
+           _raw_stream(dev)))
     return (q, s) if residual is None else (q, s, h)
 
 
@@ -519,27 +523,34 @@ def gemm_a8w8(aq: torch.Tensor, a_scale: torch.Tensor, bq: torch.Tensor, b_scale
     """C[M, N] = (aq . bq^T) * a_scale[:, None] * b_scale[None, :] (+ bias): aq int8 [M, K] with a float32 scale per
     token, bq int8 [N, K] with one per output channel (both from int8_quant, for example), bias [N] of the type of C.
     C has `out_dtype` (bf16, fp16 or fp32), or is `out` with its own type."""
-    if not aq.is_cuda or aq.dim() != 2 or bq.dim() != 2:
-        raise ValueError("aq and bq must be 2-D CUDA (HIP) tensors")
     dev = aq.get_device()
+    if dev < 0 or aq.dim() != 2 or bq.dim() != 2:
+        raise ValueError("aq and bq must be 2-D CUDA (HIP) tensors")
     M, K = aq.shape
-    N = bq.shape[0]
-    lda = _matrix(aq, "aq", torch.int8, M, K, dev)
-    ldb = _matrix(bq, "bq", torch.int8, N, K, dev)
-    ap = _vector(a_scale, "a_scale", torch.float32, M, dev)
-    bp = _vector(b_scale, "b_scale", torch.float32, N, dev)
+    N, lda, ldb = bq.shape[0], K, K
+    if not (aq.dtype is _I8 and bq.dtype is _I8 and a_scale.dtype is _F32 and b_scale.dtype is _F32
+            and aq.is_contiguous() and bq.is_contiguous() and a_scale.is_contiguous() and b_scale.is_contiguous()
+            and bq.get_device() == dev and a_scale.get_device() == dev and b_scale.get_device() == dev
+            and bq.shape[1] == K and a_scale.shape == (M,) and b_scale.shape == (N,)):
+        lda = _matrix(aq, "aq", _I8, M, K, dev)
+        ldb = _matrix(bq, "bq", _I8, N, K, dev)
+        _vector(a_scale, "a_scale", _F32, M, dev)
+        _vector(b_scale, "b_scale", _F32, N, dev)
     if out is None:
         ct = TYPES.get(out_dtype)
         if ct is None:
             raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-        out = torch.empty(M, N, dtype=out_dtype, device=aq.device)
-        ldc = N
+        out, ldc = torch.empty(M, N, dtype=out_dtype, device=aq.device), N
     else:
-        ct = _typed(out, "out")
+        ct = _typed(out, "out")[0]
         ldc = _matrix(out, "out", out.dtype, M, N, dev)
-    cp = None if bias is None else _vector(bias, "bias", out.dtype, N, dev)
+    cp = None
+    if bias is not None:
+        _vector(bias, "bias", out.dtype, N, dev)
+        cp = bias.data_ptr()
     _call((_lib or lib()).gemm_a8w8, "gemm_a8w8", dev,
-          (aq.data_ptr(), lda, ap, bq.data_ptr(), ldb, bp, cp, out.data_ptr(), ldc, ct, M, N, K, _raw_stream(dev)))
+          (aq.data_ptr(), lda, a_scale.data_ptr(), bq.data_ptr(), ldb, b_scale.data_ptr(), cp, out.data_ptr(), ldc, ct,
+           M, N, K, _raw_stream(dev)))
     return out
 
 
