@@ -232,10 +232,10 @@ __device__ __forceinline__ void store_four(const GemmArgs& p, int64_t m, int n, 
 // ---------------------------------------------------------------------------
 template <int CT, int MT, int NC, int W, int S>
 __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt) {
-  constexpr int MS = 16 * MT, NI = (NC + 15) / 16, T = 64 * W;
+  constexpr int MS = 16 * MT, NI = NC / 16, T = 64 * W;
   constexpr int UA = 2 * MT, UB = NC / 8, L = UA + UB, kRing = S * L * 1024, kSums = NI * MT * 64;
   static_assert(NI * MT <= S * L, "a wave's sums fit its ring");
-  static_assert(kSums % T == 0 || kSums < T, "whole rounds of threads");
+  static_assert(NC % 16 == 0 && (kSums % T == 0 || kSums < T), "whole fragments, whole rounds of threads");
   constexpr int kRounds = (kSums + T - 1) / T;
   __shared__ __align__(16) uint8_t lds[W * kRing];
   const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -287,8 +287,7 @@ __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt)
 #pragma unroll
       for (int i = 0; i < MT; ++i) a[kk][i] = *reinterpret_cast<const v4i*>(at + frag_at(l, kk) + 2048 * i);
 #pragma unroll
-      for (int j = 0; j < NI; ++j)  // 8 columns: the lanes of rows 8..15 read rows 0..7 again, and their sums are not used
-        b[kk][j] = *reinterpret_cast<const v4i*>(at + UA * 1024 + frag_at(NC == 8 ? l & ~8 : l, kk) + 2048 * j);
+      for (int j = 0; j < NI; ++j) b[kk][j] = *reinterpret_cast<const v4i*>(at + UA * 1024 + frag_at(l, kk) + 2048 * j);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the step is in registers: its slot is free
     load(s + S, slot);
@@ -335,14 +334,15 @@ hipError_t launch_skinny(GemmArgs& p, hipStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Ring kernel: WM x WN waves own BM x BN of C. LDS holds a ring of S stages, each the
-// operands of one 128-byte step of K; the loads of a stage are issued S-1 steps
-// before its use. One barrier per step: when it is passed, the stage has arrived for
-// every wave and the stage before it has been read by every wave.
+// operands of one 128-byte step of K; a stage is loaded again, S steps on, as soon as it
+// is read. One barrier per step, between its two 64-byte halves' matrix work: when it is
+// passed, the next stage has arrived for every wave and this one is read by every wave.
 // ---------------------------------------------------------------------------
 template <int CT, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_ring_kernel(GemmArgs p, int mt, int nt) {
   constexpr int W = WM * WN, T = 64 * W, TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
   constexpr int LA = BM / 8 / W, LB = BN / 8 / W, L = LA + LB;  // units per wave and step
+  static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0, "every wave loads whole units of both operands");
   constexpr int kStage = (BM + BN) * 128;
   using St = Strip<CT, NI>;
   using Sc = TileScales<CT, BM, BN, T>;
@@ -636,15 +636,13 @@ hipError_t launch(GemmArgs& p, hipStream_t st) {
 constexpr int64_t kMaxStride = (int64_t)1 << 22;  // 256 rows of a window stay below 2^31 bytes
 constexpr int64_t kMaxK = 131056;                 // 128 * 128 * K < 2^31
 
-}  // namespace
-
-namespace {
 int check_shape(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || N < 1 || K < 16 || K % 16 != 0 || K > kMaxK) return MXFP4_ERR_SHAPE;
   if (M > ((int64_t)1 << 24) || N > ((int64_t)1 << 24) || mxh::cdiv(M, 16) * mxh::cdiv(N, 16) > ((int64_t)1 << 30))
     return MXFP4_ERR_SHAPE;
   return MXFP4_OK;
 }
+
 }  // namespace
 
 extern "C" int gemm_a8w8_path(int64_t M, int64_t N, int64_t K) {
