@@ -86,19 +86,27 @@ __device__ __forceinline__ void store_one(const GemmArgs& p, int64_t m, int n, f
 // bytes' worth of distinct banks (with c ^ (r & 7) every read collided twice: +38 %
 // LDS cycles). Buffer-to-LDS loads fill 1 KB units of 8 rows: lane l's 16 bytes land
 // at 16*l, so lane l fetches the piece that belongs in slot l%8 of row l/8.
-__device__ __forceinline__ int unit_piece(int l, int unit_parity) { return 16 * ((l & 7) ^ (l >> 4)) ^ (64 * unit_parity); }
-__device__ __forceinline__ int frag_at(int l, int kk) { return (l & 15) * 128 + 16 * ((4 * kk + (l >> 4)) ^ ((l >> 1) & 7)); }
+__device__ __forceinline__ int unit_piece(int l, int unit_parity) {
+  return 16 * ((l & 7) ^ (l >> 4)) ^ (64 * unit_parity);
+}
+// Where lane l finds its 16 bytes of half kk of a step, in a block of 16 rows.
+__device__ __forceinline__ int frag_at(int l, int kk) {
+  return (l & 15) * 128 + 16 * ((4 * kk + (l >> 4)) ^ ((l >> 1) & 7));
+}
 
-// The buffer resource of `window` as scalar words, for the loads written in assembly.
+// A buffer resource over `rows` rows of K bytes at stride ld, as the scalar words that
+// the loads written in assembly take: an offset past the last row's end reads zeros.
 __device__ __forceinline__ u32x4 window_words(const uint8_t* base, int64_t rows, int64_t ld, int K) {
-  return u32x4{(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), (uint32_t)((rows - 1) * ld + K), 0x00020000u};
+  const uintptr_t at = (uintptr_t)base;
+  return u32x4{(uint32_t)at, (uint32_t)(at >> 32), (uint32_t)((rows - 1) * ld + K), 0x00020000u};
 }
 // 1 KB from memory to LDS (16 bytes a lane; lanes out of range write zeros). In
 // assembly: for the intrinsic the compiler waits before every LDS read that follows,
 // which would drain the ring. The kernels wait themselves (wait_loads, and a barrier
 // where other waves read). No register but m0 is written, which nothing else here uses.
 __device__ __forceinline__ void load_to_lds(uint32_t at, int voff, const u32x4& r) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(r) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(r)
+               : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {  // at most N of this wave's loads still outstanding
@@ -254,8 +262,8 @@ __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt)
     for (int u = 0; u < L; ++u) {
       const bool isA = u < UA;
       const int q = isA ? u : u - UA, k = 128 * s + unit_piece(l, q & 1);
-      load_to_lds(own0 + (slot * L + u) * 1024, s < s1 && k < p.K ? (isA ? avo + 8 * q * lda : bvo + 8 * q * ldb) + k : kOut,
-                  isA ? ar : br);
+      const int off = isA ? avo + 8 * q * lda : bvo + 8 * q * ldb;
+      load_to_lds(own0 + (slot * L + u) * 1024, s < s1 && k < p.K ? off + k : kOut, isA ? ar : br);
     }
   };
 #pragma unroll
@@ -264,7 +272,8 @@ __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt)
   float as[kRounds], bs[kRounds][4], bias[kRounds][4];
 #pragma unroll
   for (int c = 0; c < kRounds; ++c) {
-    const int t = (int)threadIdx.x + T * c, m = 16 * ((t >> 6) % MT) + (t & 15), n = 16 * ((t >> 6) / MT) + 4 * (t >> 4 & 3);
+    const int t = (int)threadIdx.x + T * c;
+    const int m = 16 * ((t >> 6) % MT) + (t & 15), n = 16 * ((t >> 6) / MT) + 4 * (t >> 4 & 3);
     as[c] = p.as[m0 + min(m, rows - 1)];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -308,7 +317,8 @@ __global__ __launch_bounds__(64 * W) void gemm_skinny_kernel(GemmArgs p, int mt)
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < kRounds; ++c) {
-    const int t = (int)threadIdx.x + T * c, m = 16 * ((t >> 6) % MT) + (t & 15), n = 16 * ((t >> 6) / MT) + 4 * (t >> 4 & 3);
+    const int t = (int)threadIdx.x + T * c;
+    const int m = 16 * ((t >> 6) % MT) + (t & 15), n = 16 * ((t >> 6) / MT) + 4 * (t >> 4 & 3);
     if (t >= kSums || m >= rows || n >= cols) continue;
     v4i sum = *reinterpret_cast<const v4i*>(lds + t * 16);
 #pragma unroll

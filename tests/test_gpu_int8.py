@@ -56,7 +56,7 @@ def codes_buffers(M, K, pad):
     return q, s
 
 
-# Every row kernel: pieces of 16 bytes up to 64, 128, 256, 512, 1024, 2048, 4096 and past, on both sides of each limit.
+# Every row kernel: pieces of 16 bytes up to 64, 128, 256, 512, 1024, 2048, 4096 and past, both sides of each limit.
 ROWS = [(1, 16), (3, 48), (6, 256), (5, 512), (4, 528), (2, 1024), (7, 1040), (2, 2048), (3, 2064), (2, 4096), (3, 4112),
         (9, 7168), (2, 8192), (3, 8208), (1, 16384), (2, 16400), (1, 32768), (2, 32784), (1, 100000)]
 
@@ -156,7 +156,8 @@ def test_rmsnorm_quant(M, K, residual, dtype):
 @pytest.mark.parametrize("M,K", [(5, 512), (6, 7168), (3, 33024)])
 def test_rmsnorm_quant_updates_the_stream_in_place(M, K, into):
     rng = np.random.default_rng(K)
-    x, r, w = values(rng, M, K, "bf16"), values(rng, M, K, "bf16"), o8.round_to(1 + 0.2 * rng.standard_normal(K), "bf16")
+    x, r = values(rng, M, K, "bf16"), values(rng, M, K, "bf16")
+    w = o8.round_to(1 + 0.2 * rng.standard_normal(K), "bf16")
     xd, rd, wd = dev(x, "bf16"), dev(r, "bf16"), dev(w[None], "bf16")[0]
     q, s = torch.empty((M, K), dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
     h = xd if into == "x" else rd

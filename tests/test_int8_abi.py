@@ -112,7 +112,7 @@ def test_path_of_a_rejected_shape(M, N, K):
         ops.a8w8_path(M, N, K)
 
 
-# Each path with row, column and K tails: K of fewer steps than the ring's stages, of many, and tails of 16 to 112 bytes.
+# Each path with row, column and K tails: K of fewer steps than the ring's stages and of many, tails of 16 to 112.
 PATH_SHAPES = [("skinny_16x16", 17, 33, 144), ("skinny_16x16", 15, 1001, 7184), ("skinny_32x16", 17, 2050, 528),
                ("skinny_32x16", 31, 3000, 7120), ("skinny_32x32", 33, 2050, 1040), ("skinny_32x32", 17, 4100, 2096),
                ("ring_32x32", 17, 33, 16), ("ring_32x32", 33, 257, 16), ("ring_32x32", 33, 2051, 784),

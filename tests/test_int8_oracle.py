@@ -55,7 +55,8 @@ def test_rmsnorm_against_fractions():
             # inv 2^-24 (and the float64 steps), the products 2^-24 each
             want = float(h[i, k]) / float(ms) ** 0.5 * float(w[k])
             assert abs(float(y[i, k]) - want) <= abs(want) * (3 * 2.0 ** -24 + 2.0 ** -40)
-            assert abs(float(h[i, k]) - (float(x[i, k]) + float(r[i, k]))) <= 2.0 ** -8 * abs(float(h[i, k])) + 2.0 ** -134
+            total = float(x[i, k]) + float(r[i, k])
+            assert abs(float(h[i, k]) - total) <= 2.0 ** -8 * abs(total) + 2.0 ** -134
 
 
 def test_gemm_against_fractions():
@@ -65,6 +66,7 @@ def test_gemm_against_fractions():
     c = o8.gemm(aq, a_s, bq, b_s)
     for m in range(3):
         for n in range(4):
-            want = Fraction(sum(int(a) * int(b) for a, b in zip(aq[m], bq[n]))) * Fraction(float(a_s[m])) * Fraction(float(b_s[n]))
+            acc = sum(int(a) * int(b) for a, b in zip(aq[m], bq[n]))
+            want = acc * Fraction(float(a_s[m])) * Fraction(float(b_s[n]))
             assert abs(Fraction(float(c[m, n])) - want) <= abs(want) * Fraction(4, 2 ** 24)
     assert np.allclose(o8.gemm_f64(aq, a_s, bq, b_s), c, rtol=2.0 ** -21, atol=0)
