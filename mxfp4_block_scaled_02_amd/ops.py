@@ -415,8 +415,9 @@ A8W8_PATHS = dict(enumerate(["skinny_16x16", "skinny_32x16", "skinny_32x32", "ri
 # kept short too: the raw handle of the current stream spares building a Stream, and one chain of tests passes the
 # ordinary call (everything contiguous); what fails it goes through the checks below, which either say what is wrong
 # or find the strides.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (Both names are absent from a torch built without devices, where every tensor is refused before their use.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _I8, _F32 = torch.int8, torch.float32
 
 
