@@ -222,7 +222,8 @@ def check_gemm(rng, M, N, K, dtype="bf16", bias=False, pads=(0, 0, 0), full=Fals
     assert (np.abs(got - want) <= np.abs(want) * eps + size * (1 + eps) * 4 * 2.0 ** -24 + tiny).all()
 
 
-# Both sides of every tile extent and of the row counts where the kernel changes, K inside a step and over many.
+# Small products with extents around the tiles', K inside a step and over many; they take the skinny kernels and the
+# ring tiles to 64 x 64 (PATH_SHAPES reaches every kernel, test_gpu_int8_kernels.py with every type).
 SHAPES = [(1, 1, 16), (1, 16, 64), (4, 256, 512), (3, 17, 48), (16, 33, 128), (17, 15, 144), (16, 264, 7168),
           (1, 100, 8192), (32, 130, 2064), (33, 70, 1040), (48, 257, 528), (64, 64, 256), (65, 129, 272), (100, 31, 4096),
           (127, 255, 400), (128, 256, 1024), (129, 257, 1040), (200, 512, 2048), (255, 300, 96), (256, 256, 128),
