@@ -192,7 +192,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void row_kernel(RowArgs a) {
   __shared__ uint32_t part_max[W];
   const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t group = (int64_t)blockIdx.y * kGridX + blockIdx.x;
-  const int64_t row = W == 1 ? group * 4 + (threadIdx.x >> 6) : group;
+  // a wave's row is uniform; without saying so the loads below loop over their lanes' descriptors
+  const int64_t row = W == 1 ? group * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : group;
   if (row >= a.M) return;  // whole workgroups; with W == 1 whole waves, and then there is no barrier
   const int bytes = a.K * P::kSize;
   const __amdgpu_buffer_rsrc_t xr = row_rsrc(a.x + row * a.ldx, bytes);
