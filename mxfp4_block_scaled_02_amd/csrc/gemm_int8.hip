@@ -103,11 +103,14 @@ __device__ __forceinline__ u32x4 window_words(const uint8_t* base, int64_t rows,
 // 1 KB from memory to LDS (16 bytes a lane; lanes out of range write zeros). In
 // assembly: for the intrinsic the compiler waits before every LDS read that follows,
 // which would drain the ring. The kernels wait themselves (wait_loads, and a barrier
-// where other waves read). The LDS address goes in m0 as an operand: the compiler writes
-// the register itself and knows what it holds (a move inside the block, which it would not
-// know of, left any later use of m0 with this address). One wait state between the two.
+// where other waves read). The LDS address goes to m0, which is an output, so that the
+// compiler does not count on what it had there itself. (As an input that it writes itself,
+// loads of the large kernel came closer together: 350 cycles of latency for 240, +0.5 % time.)
 __device__ __forceinline__ void load_to_lds(uint32_t at, int voff, const u32x4& r) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(at), "v"(voff), "s"(r)
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+               : "={m0}"(m0)
+               : "s"(at), "v"(voff), "s"(r)
                : "memory");
 }
 template <int N>
