@@ -7,15 +7,16 @@
 // neighbouring columns of C. K goes in steps of 128 bytes, a cache line of a row,
 // and operands reach LDS by loads that bypass the registers.
 //
-// Three kernels, chosen from (M, N, K) by a model of their times (kTiles below):
+// Three kernels, chosen from (M, N, K) by a ranking of them (kTiles below):
 //  * skinny: 16 or 32 rows x 16 or 32 columns, K split over four waves (few tokens);
 //  * ring: 32 x 32 to 128 x 256 tiles, a ring of LDS stages;
 //  * large: 256 x 256 tiles, a ring of finer units, more under way per CU.
-// What bounds them: a CU takes in 60 to 70 GB/s of operands (45 to 85 lines under way at
-// 250 to 330 cycles each, whatever the order of the requests), so up to a thousand rows
-// the bytes per CU decide (M256 N4096 K7168, 917 KB a CU: 14.3 us, 1.05 POP/s); a whole
-// chip of 256 x 256 tiles is held by the power limit (M4096 N4096 K7168: 87 us, 2.75
-// POP/s; 75 us on codes of zero).
+// What bounds them: the ring kernels take in 54 to 66 GB/s of operands a CU over their
+// whole time (76 to 85 lines under way at 315 to 330 cycles each; a loop of such loads
+// alone 55 to 75), so up to a thousand rows the bytes per CU decide (M256 N4096 K7168,
+// 917 KB a CU: 13.8 to 15 us with the operands in the Infinity Cache, 1.0 to 1.1 POP/s,
+// and 19 us from memory); a whole chip of 256 x 256 tiles is held by the power limit (M4096
+// N4096 K7168: 86 to 91 us, 2.65 to 2.8 POP/s, from memory 90 to 95; on codes of zero 75).
 #include "host_common.hpp"
 #include "mx_device.hpp"
 
@@ -588,15 +589,22 @@ hipError_t launch_large(GemmArgs& p, hipStream_t st) {
   return hipLaunchKernel((const void*)gemm_large_kernel<CT>, dim3((unsigned)(mt * nt)), dim3(512), args, 0, st);
 }
 
-// The kernels a call may take, and an estimate of each one's time in us as a function
-// of its tiles per CU n (rounded up over kModelCUs) and 128-byte steps of K t:
+// The kernels a call may take, and a figure that ranks them as a function of a kernel's
+// tiles per CU n (rounded up over kModelCUs) and 128-byte steps of K t:
 //   start + tile * n + step * t + tile_step * n * t.
-// The figures are least-squares fits of relative error to 255 measured shapes (M 1 to
-// 4096, N 256 to 7168, K 512 to 7168, cold operands, graph replay). Over those shapes
-// the choice costs 1.1 % more than always taking the fastest kernel (at most 25 %, M4096
-// N2112 K512). What decides: below about 200 tiles the chip idles, so small tiles win
-// (M16 N2112 K7168: 8.5 us on 16 x 16, 19 on 64 x 64); past it the bytes per CU do, as
-// BM + BN per BM * BN (M1024 N4096 K7168: 41 us on 128 x 128, 63 on 64 x 64).
+// The constants are least-squares fits of relative error to times in us over 255 shapes (M
+// 1 to 4096, N 256 to 7168, K 512 to 7168, operands from memory, graph replay;
+// profiles/int8_tile_fit.csv). The figure is not the time: it has no term for the memory
+// that all tiles read, which falls out where it is the same for all of them. For the kernel
+// taken it is 0.63 to 1.27 of the time over these shapes, and 0.46 to 1.13 (median 0.66)
+// with N or K of 8192 to 28672, where reading the weight bounds a call of few rows.
+// The choice, over every kernel measured on every shape (profiles/int8_tile_check.csv),
+// costs 0.8 % more than always taking the fastest on the 255 shapes (at most 23 %, M4096
+// N2112 K512: 16.4 us on 256 x 256, 13.3 on 128 x 64) and 1.0 % on 36 shapes with the
+// larger extents (at most 11 %, M1 N28672 K8192: 47.6 us on the 32 x 32 ring, 42.8 on 16 x 16).
+// What decides: below about 200 tiles the chip idles, so small tiles win (M16 N2112 K7168:
+// 7.7 us on 16 x 16, 17.0 on 64 x 64); past it the bytes per CU do, as BM + BN per BM * BN
+// (M1024 N4096 K7168: 36.9 us on 128 x 128, 58.2 on 64 x 64).
 struct TileModel {
   int bm, bn;
   float start, tile, step, tile_step;

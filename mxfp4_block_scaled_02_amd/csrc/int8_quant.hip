@@ -12,9 +12,10 @@
 // A row is read once: thread t of the row's threads takes the 16-byte pieces t,
 // t + threads, ..., keeps them in registers, and between the reductions (sum of
 // squares, maximum) nothing goes to memory. The bytes bound it from about a thousand
-// rows on: M4096 K7168 bf16 with a residual, 205 MB, 33 us in the kernel (6.2 TB/s; a
-// large copy reaches 5.4), without norm, 88 MB, 14.2 us. A few rows take one trip to
-// memory and two reductions: 16 rows 3.9 us in a graph, of which the launch is 1.7.
+// rows on: M4096 K7168 bf16 with a residual, 205 MB, 39 us with everything from memory
+// (5.3 TB/s; a large copy reaches 5.4), without norm, 88 MB, 17.5 us; 31.5 and 14.6 us
+// where the Infinity Cache holds part of it. A few rows take one trip to memory and two
+// reductions: 16 rows 3.7 us in a graph, of which the launch is 1.7.
 #include "host_common.hpp"
 #include "mx_device.hpp"
 
@@ -270,7 +271,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void row_kernel(RowArgs a) {
 
 // Rows longer than the registers of a workgroup hold: one workgroup to a row,
 // which reads the row again for each of its phases. With a residual the first
-// phase writes h and the later ones read it back, each thread its own pieces.
+// phase writes h and the later ones read it back, each thread its own pieces. Quantising
+// 4096 bf16 rows of K 36864 takes 103 us (4.4 TB/s; the last length that the registers
+// hold, K 32768, 71 us, 5.6 TB/s), 8192 fp32 rows of K 28672 297 us (4.0 TB/s).
 constexpr int kLongWaves = 16;
 template <int DT, int MODE>
 __global__ __launch_bounds__(64 * kLongWaves) void row_long_kernel(RowArgs a) {
@@ -335,12 +338,14 @@ hipError_t launch_row(RowArgs& a, hipStream_t st) {
                          dim3(W == 1 ? 256 : 64 * W), args, 0, st);
 }
 
-// Waves to a row and pieces to a thread: the fewest waves that leave a thread one or two
-// pieces, measured over K 256 to 16384, 16 to 4096 rows, bf16 and fp32. More waves than
-// that cost their barriers and leave the last ones empty (quantising 2112 rows of 1792
-// fp32 pieces: 16 waves 16.9 us, 8 waves 14.8; norm of 4096 rows of 258 bf16 pieces: 16
-// waves 31.8 us, 4 waves 15.4), fewer give a thread more pieces to add up in turn (norm of
-// 16 rows of 896 pieces: 2 waves 4.8 us, 8 waves 3.9).
+// Waves to a row and pieces to a thread, by the row's pieces; both were measured over K 256
+// to 16384, 16 to 4096 rows, bf16 and fp32. Up to 1024 pieces a thread has one or two: more
+// pieces are added up in turn (norm of 16 rows of 896 pieces: 2 waves 4.8 us, 8 waves 3.9),
+// more waves cost their barriers and leave the last ones empty (norm of 4096 rows of 258
+// bf16 pieces: 16 waves 31.8 us, 4 waves 15.4). Two waves with one piece rather than one
+// with two take 65 to 128 pieces (norm of 16 rows of 128: 3.12 us, 3.26). Past 1024 pieces a
+// thread has four: eight waves as long as they hold the row (quantising 2112 rows of 1792
+// fp32 pieces: 16 waves with two 16.9 us, 8 waves with four 14.8).
 template <int DT, int MODE>
 hipError_t launch_mode(RowArgs& a, hipStream_t st) {
   const int pieces = a.K / Piece<DT>::kElems;
