@@ -466,6 +466,101 @@ int gemm_a8w8(const void* Aq, int64_t lda, const float* as, const void* Bq, int6
 #define MXFP4_A8W8_PATHS 10
 int gemm_a8w8_path(int64_t M, int64_t N, int64_t K);
 
+/* ---------------------------------------------------------------------------
+ * Products whose weight is picked row by row: a mixture of experts (router and
+ * experts) for a few tokens, and low-rank adapters beside a shared projection.
+ * Indices lie in device memory, so no call can refuse one: an expert or adapter
+ * index outside its range means "none" wherever it is read. A row's result
+ * depends on nothing but the row's own data and the weights it picks: not on
+ * the other rows, nor on how work is split between workgroups.
+ * Unlike the calls above, rows that are not finite stay by themselves: what an
+ * Inf or NaN in one row of the activations gives is unspecified in that row of the
+ * output (not finite, as a rule) and changes no other row.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * moe_route -- the k experts of each token and their weights, from the router's
+ * logits l[E] of the token:
+ *   score : softmax (MXFP4_SCORE_SOFTMAX) exp(l[e] - max l) / sum exp(l - max l), or
+ *           sigmoid (MXFP4_SCORE_SIGMOID) 1 / (1 + exp(-l[e])), each within a few
+ *           float64 roundings.
+ *   rank  : l[e] without a bias, else score[e] + bias[e] in float64. An expert
+ *           whose logit is -Inf, or whose rank is -Inf, is never chosen.
+ *   ids[t, 0..k)     : the experts of largest rank in falling order, equal ranks
+ *           by rising index; -1 where fewer than k can be chosen.
+ *   weights[t, 0..k) : fp32 of scale * score (bias not included), divided by the
+ *           sum of the chosen scores if `renormalize` is not zero (a sum of zero
+ *           gives zeros); 0 where the id is -1.
+ *   A row with a NaN or a +Inf among its logits or ranks gets the ids 0, 1, ..., k-1
+ *   and the weights NaN, so that what is computed from it shows it.
+ *   logits : [T, E] of type `dtype` (MXFP4_TYPE_*), row stride ldl >= E elements,
+ *            aligned to its element.
+ *   bias   : fp32 [E], or NULL.
+ *   weights: out, fp32 [T, k]; ids: out, int32 [T, k]; both contiguous.
+ *   1 <= T <= 2^24, 1 <= E <= 1024, 1 <= k <= min(E, 64); ldl <= 2^36; scale finite
+ *   (else MXFP4_ERR_ARG).
+ * ------------------------------------------------------------------------- */
+#define MXFP4_SCORE_SOFTMAX 0
+#define MXFP4_SCORE_SIGMOID 1
+int moe_route(const void* logits, int64_t ldl, int dtype, const float* bias, int score, int renormalize, float scale,
+              float* weights, int32_t* ids, int64_t T, int64_t E, int64_t k, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_a16w4 -- the experts' gated MLP for a few tokens, bf16 activations on MXFP4
+ * weights (weight-only: x is not quantised, as the weights' bytes bound the
+ * call):
+ *   for each pair (t, j) with 0 <= e = ids[t, j] < E:
+ *     g = x[t] . W13[e][0..I)^T,  u = x[t] . W13[e][I..2I)^T     (fp32 sums)
+ *     h = g / (1 + exp(-g)) * u                                  (fp32)
+ *   y[t] = bf16(sum_j weights[t, j] * (h . W2[e]^T))             (fp32 sums)
+ * Weight products and sums are fp32 (weights dequantise to bf16 exactly for scale
+ * bytes 1 to 252). A token without a valid pair gets y = 0; the same expert twice
+ * in a token counts twice. Pairs of weight 0 are computed like the others.
+ *   x   : bf16 [T, H], row stride ldx >= H elements; x and ldx * 2 multiples of
+ *         16 bytes; ldx <= 2^36.
+ *   ids : int32 [T, k]; weights: fp32 [T, k]; contiguous.
+ *   w13 : [E] packed weights of 2I x H (gate rows, then up rows), each as
+ *         mxfp4_pack_B leaves it, stride13 bytes apart (>= mxfp4_pack_B_bytes(2I, H)).
+ *   w2  : [E] packed weights of H x I, stride2 bytes apart (>= mxfp4_pack_B_bytes(H, I)).
+ *         w13, w2 and both strides multiples of 16 bytes; strides <= 2^40.
+ *   y   : out, bf16 [T, H], row stride ldy >= H elements, 8-byte aligned, ldy % 4
+ *         == 0, ldy <= 2^36. No overlap with any other argument.
+ *   H, I multiples of 32, 32 <= H, I <= 2^20; 1 <= E <= 1024; 1 <= k; T >= 1;
+ *   T * k <= MXFP4_MOE_MAX_PAIRS. More tokens are the grouped calls' work, on the
+ *   same packed weights.
+ *   workspace : >= moe_a16w4_workspace_bytes(T, k, H, I), 16-byte aligned,
+ *         any contents; scratch during the call only. (0 for a rejected shape.)
+ * ------------------------------------------------------------------------- */
+#define MXFP4_MOE_MAX_PAIRS 4096
+size_t moe_a16w4_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
+int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const float* weights, const void* w13, int64_t stride13,
+              const void* w2, int64_t stride2, void* y, int64_t ldy, int64_t T, int64_t k, int64_t E, int64_t H,
+              int64_t I, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * lora_add -- low-rank adapters of many requests, added in place to a shared
+ * projection's product:
+ *   i = index[t];  y[t] = Ty(y[t] + scale[i] * ((x[t] . A[i]^T) . B[i]^T))
+ * for rows with 0 <= i < n; other rows of y are neither read nor written. Sums are
+ * fp32; x . A^T is held as a sum of 16-bit pieces for the second product (two, or
+ * three where y is fp32: within 2^-16 or 2^-23 of the value).
+ *   y : in/out, [T, N] of type ytype (xtype or MXFP4_TYPE_F32), row stride ldy >= N
+ *       elements, aligned to its element; ldy <= 2^36.
+ *   x : [T, K] of type xtype (MXFP4_TYPE_BF16 or _F16), row stride ldx >= K.
+ *   a : [n, R, K] and b : [n, N, R] of type xtype, contiguous.
+ *       x, ldx * 2 bytes, a and b multiples of 16 bytes; ldx <= 2^36.
+ *   index : int32 [T];  scale : fp32 [n], or NULL for 1.
+ *   T, n >= 1, T <= 2^20, n <= 2^20; K % 8 == 0, 8 <= K <= 2^20; R % 8 == 0,
+ *   8 <= R <= 128; 1 <= N <= 2^20. y overlaps no other argument. Adapters of
+ *   smaller rank are padded with rows (A) and columns (B) of zeros.
+ *   workspace : >= lora_add_workspace_bytes(T, K, R), 16-byte aligned, any
+ *       contents; scratch during the call only. (0 for a rejected shape.)
+ * ------------------------------------------------------------------------- */
+size_t lora_add_workspace_bytes(int64_t T, int64_t K, int64_t R);
+int lora_add(void* y, int64_t ldy, int ytype, const void* x, int64_t ldx, int xtype, const void* a, const void* b,
+             const int32_t* index, const float* scale, int64_t T, int64_t N, int64_t K, int64_t R, int64_t n,
+             void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

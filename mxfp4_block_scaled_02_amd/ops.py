@@ -28,7 +28,8 @@ EXPORTED = ["mxfp4_status_str", "mxfp4_quant", "mxfp4_rmsnorm_quant", "mxfp4_pac
             "gemm_a4w4_fused_dump",
             "gemm_a4w4", "grouped_gemm_a4w4_workspace_bytes", "grouped_gemm_a4w4", "grouped_gemm_a4w4_dump_bytes",
             "grouped_gemm_a4w4_dump_copies", "grouped_gemm_a4w4_dump", "grouped_gemm_a4w4_mnk", "grouped_gemm_nvfp4",
-            "int8_quant", "int8_rmsnorm_quant", "gemm_a8w8", "gemm_a8w8_path"]
+            "int8_quant", "int8_rmsnorm_quant", "gemm_a8w8", "gemm_a8w8_path", "moe_route", "moe_a16w4_workspace_bytes",
+            "moe_a16w4", "lora_add_workspace_bytes", "lora_add"]
 
 
 class Mxfp4Error(RuntimeError):
@@ -109,6 +110,14 @@ def lib() -> ctypes.CDLL:
         L.gemm_a8w8.argtypes = [vp, i64, vp, vp, i64, vp, vp, vp, i64, i32, i64, i64, i64, vp]
         L.gemm_a8w8.restype = i32
         L.gemm_a8w8_path.argtypes, L.gemm_a8w8_path.restype = [i64, i64, i64], i32
+        L.moe_route.argtypes = [vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, i64, i64, i64, vp]
+        L.moe_route.restype = i32
+        L.moe_a16w4_workspace_bytes.argtypes, L.moe_a16w4_workspace_bytes.restype = [i64] * 4, sz
+        L.moe_a16w4.argtypes = [vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, sz, vp]
+        L.moe_a16w4.restype = i32
+        L.lora_add_workspace_bytes.argtypes, L.lora_add_workspace_bytes.restype = [i64] * 3, sz
+        L.lora_add.argtypes = [vp, i64, i32, vp, i64, i32, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, sz, vp]
+        L.lora_add.restype = i32
         _lib = L
         return L
 
@@ -562,3 +571,132 @@ def a8w8_path(M: int, N: int, K: int) -> str:
     if p not in A8W8_PATHS:
         raise ValueError(f"gemm_a8w8 rejects M={M} N={N} K={K}")
     return A8W8_PATHS[p]
+
+
+# Products whose weight is picked row by row. Their scratch is allocated for each call (its contents do not matter): a
+# captured graph then holds its own, and graphs that are replayed at the same time do not meet in it.
+SCORES = {"softmax": 0, "sigmoid": 1}
+_I32, _U8, _BF16 = torch.int32, torch.uint8, torch.bfloat16
+
+
+def _scratch(nbytes: int, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=_U8, device=like.device)
+
+
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
+    """Checks a contiguous argument of a given shape."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on device {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "softmax",
+              renormalize: bool = True, scale: float = 1.0, out=None):
+    """The k experts of each token and their weights from a router's logits [T, E] (bf16, fp16 or fp32):
+    (weights float32 [T, k], ids int32 [T, k]), by falling rank, ties to the lower index, -1 and 0 where nothing is left
+    to choose (logits of -inf). The rank is the logit, or score + bias with a float32 bias [E]; the weights are
+    scale * score, over their sum if `renormalize`. `out` = (weights, ids) reuses given buffers."""
+    dt, dev, T, E = _typed(logits, "logits")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {list(SCORES)}, got {score!r}")
+    ldl = E if logits.is_contiguous() else _matrix(logits, "logits", logits.dtype, T, E, dev)
+    bp = None
+    if bias is not None:
+        _vector(bias, "bias", _F32, E, dev)
+        bp = bias.data_ptr()
+    if out is None:
+        if k < 1:
+            raise ValueError(f"k must be at least 1, got {k}")
+        device = logits.device
+        weights, ids = torch.empty(T, k, dtype=_F32, device=device), torch.empty(T, k, dtype=_I32, device=device)
+    else:
+        weights, ids = out
+        _dense(weights, "weights", _F32, (T, k), dev)
+        _dense(ids, "ids", _I32, (T, k), dev)
+    _call((_lib or lib()).moe_route, "moe_route", dev,
+          (logits.data_ptr(), ldl, dt, bp, SCORES[score], bool(renormalize), float(scale), weights.data_ptr(),
+           ids.data_ptr(), T, E, k, _raw_stream(dev)))
+    return weights, ids
+
+
+def pack_experts(bq: torch.Tensor, bs: torch.Tensor) -> torch.Tensor:
+    """pack_B of each expert's weight: fp4x2 [E, N, K/2] and E8M0 [E, N, K/32] (contiguous uint8) -> packed uint8
+    [E, pack_B_bytes(N, K)]. Row e is expert e's packed B, for moe_a16w4 and for the grouped calls alike."""
+    if bq.dim() != 3 or bs.dim() != 3 or bq.shape[0] != bs.shape[0]:
+        raise ValueError("bq must be [E, N, K/2] and bs [E, N, K/32]")
+    return torch.stack([pack_B(q, s) for q, s in zip(bq, bs)])
+
+
+def _experts(p: torch.Tensor, name: str, N: int, K: int, dev: int):
+    """(number of experts, bytes from one to the next) of packed expert weights."""
+    need = pack_B_bytes(N, K)
+    if (p.dtype is not _U8 or p.get_device() != dev or p.dim() != 2 or need == 0 or p.shape[1] < need
+            or p.stride(1) != 1):
+        raise ValueError(f"{name} must be uint8 [E, {need}] (pack_experts of {N} x {K}) on device {dev}, "
+                         f"got {p.dtype} {list(p.shape)} on {p.device}")
+    return p.shape[0], p.stride(0) if p.shape[0] > 1 else p.shape[1]
+
+
+def moe_a16w4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, I: int,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """The experts' gated MLP for a few tokens: y[t] = sum_j weights[t, j] * W2_e (silu(G_e x[t]) * (U_e x[t])) with
+    e = ids[t, j]; ids outside [0, E) are left out. x bf16 [T, H], ids int32 and weights float32 [T, k] (from moe_route,
+    for example), w13 and w2 from pack_experts: [E] weights of 2I x H (gate rows G, then up rows U) and of H x I.
+    Returns bf16 [T, H], or `out`."""
+    dev = x.get_device()
+    if dev < 0 or x.dim() != 2:
+        raise ValueError("x must be a 2-D CUDA (HIP) tensor")
+    T, H = x.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    k = ids.shape[1]
+    ldx = H if x.dtype is _BF16 and x.is_contiguous() else _matrix(x, "x", _BF16, T, H, dev)
+    _dense(ids, "ids", _I32, (T, k), dev)
+    _dense(weights, "weights", _F32, (T, k), dev)
+    E, stride13 = _experts(w13, "w13", 2 * I, H, dev)
+    E2, stride2 = _experts(w2, "w2", H, I, dev)
+    if E != E2:
+        raise ValueError(f"w13 has {E} experts and w2 {E2}")
+    if out is None:
+        out, ldy = torch.empty(T, H, dtype=_BF16, device=x.device), H
+    else:
+        ldy = _matrix(out, "out", _BF16, T, H, dev)
+    L = _lib or lib()
+    nbytes = L.moe_a16w4_workspace_bytes(T, k, H, I)
+    ws = _scratch(nbytes, x)
+    _call(L.moe_a16w4, "moe_a16w4", dev,
+          (x.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), w13.data_ptr(), stride13, w2.data_ptr(), stride2,
+           out.data_ptr(), ldy, T, k, E, H, I, ws.data_ptr(), nbytes, _raw_stream(dev)))
+    return out
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
+             scale: torch.Tensor | None = None) -> torch.Tensor:
+    """Low-rank adapters of many requests, added in place to a shared projection's product y [T, N]:
+    y[t] += scale[i] * (x[t] . a[i]^T) . b[i]^T with i = index[t]; rows whose index is outside [0, n) stay as they are.
+    x [T, K], a [n, R, K] and b [n, N, R] bf16 or fp16, y of that type or float32, index int32 [T], scale float32 [n].
+    Returns y."""
+    yt, dev, T, N = _typed(y, "y")
+    if x.dim() != 2 or a.dim() != 3:
+        raise ValueError("x must be [T, K] and a [n, R, K]")
+    D, K = x.dtype, x.shape[1]
+    n, R = a.shape[0], a.shape[1]
+    ldy = N if y.is_contiguous() else _matrix(y, "y", y.dtype, T, N, dev)
+    if not (x.get_device() == dev and x.shape[0] == T and x.is_contiguous()):
+        ldx = _matrix(x, "x", D, T, K, dev)
+    else:
+        ldx = K
+    _dense(a, "a", D, (n, R, K), dev)
+    _dense(b, "b", D, (n, N, R), dev)
+    _vector(index, "index", _I32, T, dev)
+    sp = None
+    if scale is not None:
+        _vector(scale, "scale", _F32, n, dev)
+        sp = scale.data_ptr()
+    L = _lib or lib()
+    nbytes = L.lora_add_workspace_bytes(T, K, R)
+    ws = _scratch(nbytes, x)
+    _call(L.lora_add, "lora_add", dev,
+          (y.data_ptr(), ldy, yt, x.data_ptr(), ldx, TYPES.get(D, -1), a.data_ptr(), b.data_ptr(), index.data_ptr(), sp,
+           T, N, K, R, n, ws.data_ptr(), nbytes, _raw_stream(dev)))
+    return y
