@@ -470,9 +470,11 @@ int gemm_a8w8_path(int64_t M, int64_t N, int64_t K);
  * Products whose weight is picked row by row: a mixture of experts (router and
  * experts) for a few tokens, and low-rank adapters beside a shared projection.
  * Indices lie in device memory, so no call can refuse one: an expert or adapter
- * index outside its range means "none" wherever it is read. A row's result
- * depends on nothing but the row's own data and the weights it picks: not on
- * the other rows, nor on how work is split between workgroups.
+ * index outside its range means "none" wherever it is read. The same call gives
+ * the same result bit for bit, and a row's result takes in nothing but the row's own
+ * data and the weights it picks. (moe_route and moe_a16w4: the same bits whatever the
+ * other rows are; lora_add: the order of its fp32 sums goes by T and by how many of
+ * 64 neighbouring rows have the adapter.)
  * Unlike the calls above, rows that are not finite stay by themselves: what an
  * Inf or NaN in one row of the activations gives is unspecified in that row of the
  * output (not finite, as a rule) and changes no other row.
