@@ -472,9 +472,9 @@ int gemm_a8w8_path(int64_t M, int64_t N, int64_t K);
  * Indices lie in device memory, so no call can refuse one: an expert or adapter
  * index outside its range means "none" wherever it is read. The same call gives
  * the same result bit for bit, and a row's result takes in nothing but the row's own
- * data and the weights it picks. (moe_route and moe_a16w4: the same bits whatever the
- * other rows are; lora_add: the order of its fp32 sums goes by T and by how many of
- * 64 neighbouring rows have the adapter.)
+ * data and the weights it picks. The order of a row's fp32 sums goes by the sizes and
+ * by the indices of the call (for moe_route it is always the same), so its last bit may
+ * differ between batches.
  * Unlike the calls above, rows that are not finite stay by themselves: what an
  * Inf or NaN in one row of the activations gives is unspecified in that row of the
  * output (not finite, as a rule) and changes no other row.
@@ -513,10 +513,10 @@ int moe_route(const void* logits, int64_t ldl, int dtype, const float* bias, int
  * call):
  *   for each pair (t, j) with 0 <= e = ids[t, j] < E:
  *     g = x[t] . W13[e][0..I)^T,  u = x[t] . W13[e][I..2I)^T     (fp32 sums)
- *     h = g / (1 + exp(-g)) * u                                  (fp32)
- *   y[t] = bf16(sum_j weights[t, j] * (h . W2[e]^T))             (fp32 sums)
- * Weight products and sums are fp32 (weights dequantise to bf16 exactly for scale
- * bytes 1 to 252). A token without a valid pair gets y = 0; the same expert twice
+ *     h = weights[t, j] * g / (1 + exp(-g)) * u                  (fp32, kept within 2^-17)
+ *   y[t] = bf16(sum_j h . W2[e]^T)                               (fp32 sums)
+ * MXFP4 weights dequantise to bf16 exactly for scale bytes 1 to 252; bytes 253 to 255
+ * (values past the type, NaN) give an unspecified y. A token without a valid pair gets y = 0; the same expert twice
  * in a token counts twice. Pairs of weight 0 are computed like the others.
  *   x   : bf16 [T, H], row stride ldx >= H elements; x and ldx * 2 multiples of
  *         16 bytes; ldx <= 2^36.

@@ -4,6 +4,8 @@
 #include "host_common.hpp"
 #include "mx_device.hpp"
 
+#pragma clang fp contract(off)
+
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -13,6 +15,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxE = 1024;
+constexpr int kNonTemporal = 2;  // the nt bit of the buffer instructions
 
 struct MoeArgs {
   const uint8_t* x;  // strides in bytes
@@ -25,7 +28,7 @@ struct MoeArgs {
   int64_t stride2;
   uint8_t* y;
   int64_t ldy;
-  uint8_t* h;   // bf16 [pairs, I]
+  uint8_t* h;   // bf16 [2, pairs, I]
   float* part;  // fp32 [pairs, H]
   int T, k, E, H, I;
 };
@@ -45,41 +48,79 @@ __device__ __forceinline__ Packed packed(const uint8_t* base, int N, int K) {
   return p;
 }
 
-// The expert of a slot (the slot-th of those that any pair takes, in rising order), and its
-// pairs. Returns the number of pairs, 0 for a slot past the last expert.
+// The pairs (t, j) of a slot's expert. A launch has a slot for each expert that could be
+// taken: for each pair (up to 64 pairs), else for each expert where there are as many pairs as
+// experts (slot_is_expert: the expert is known at once), else for as many experts as there are
+// pairs. `list` has the slot's pairs in an order that the ids alone decide. Returns their
+// number, 0 for a slot to skip.
 struct Rows {
   uint32_t bits[kMaxE / 32];
-  int count;
-  uint16_t pair[MXFP4_MOE_MAX_PAIRS];
+  int count[kWaves];
+  uint16_t list[MXFP4_MOE_MAX_PAIRS];
 };
+__device__ __forceinline__ bool slot_is_expert(const MoeArgs& a) { return a.T * a.k > 64 && a.T * a.k >= a.E; }
 __device__ __forceinline__ int find_rows(const MoeArgs& a, int slot, Rows& s, int& expert) {
   const int tid = threadIdx.x, l = tid & 63, P = a.T * a.k;
-  if (tid < kMaxE / 32) s.bits[tid] = 0;
-  if (tid == 0) s.count = 0;
-  __syncthreads();
-  for (int i = tid; i < P; i += kThreads) {
-    const uint32_t e = (uint32_t)a.ids[i];
-    if (e < (uint32_t)a.E) atomicOr(&s.bits[e >> 5], 1u << (e & 31));
+  if (P <= 64) {
+    // A slot for each pair, which goes on if it is the first with its expert.
+    const int id = l < P ? a.ids[l] : -1;
+    expert = __builtin_amdgcn_readlane(id, slot);
+    const uint64_t mine = __ballot(id == expert);
+    if ((uint32_t)expert >= (uint32_t)a.E || __ffsll((unsigned long long)mine) - 1 != slot) return 0;
+    if (tid < 64 && id == expert) s.list[__popcll(mine & (((uint64_t)1 << l) - 1))] = (uint16_t)l;
+    __syncthreads();
+    return __popcll(mine);
   }
-  __syncthreads();
-  const uint32_t word = l < kMaxE / 32 ? s.bits[l] : 0;
-  int upto = __popc(word);  // experts in this and the words before
+  // A thread's ids stay in registers from one pass to the next (4096 pairs: 16 to a thread).
+  constexpr int kEach = MXFP4_MOE_MAX_PAIRS / kThreads;
+  const int wave = tid >> 6, each = (P + kThreads - 1) / kThreads;
+  uint32_t id[kEach];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(upto, d, 64);
-    if (l >= d) upto += o;
+  for (int i = 0; i < kEach; ++i)
+    id[i] = i < each && tid + kThreads * i < P ? (uint32_t)a.ids[tid + kThreads * i] : ~0u;
+  if (slot_is_expert(a)) {
+    expert = slot;
+  } else {  // the slot-th of the experts that any pair takes, in rising order
+    if (tid < kMaxE / 32) s.bits[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (i < each && id[i] < (uint32_t)a.E) atomicOr(&s.bits[id[i] >> 5], 1u << (id[i] & 31));
+    __syncthreads();
+    const uint32_t word = l < kMaxE / 32 ? s.bits[l] : 0;
+    int before = 0, at = 0;  // experts before word `at`
+    uint32_t w = 0;
+    for (; at < kMaxE / 32; ++at) {
+      w = (uint32_t)__builtin_amdgcn_readlane((int)word, at);
+      if (before + __popc(w) > slot) break;
+      before += __popc(w);
+    }
+    if (at == kMaxE / 32) return 0;  // the same on every thread
+    const bool mine = l < 32 && (w >> l & 1) && __popc(w & ((1u << l) - 1)) == slot - before;
+    expert = 32 * at + __ffsll((unsigned long long)__ballot(mine)) - 1;
   }
-  const uint64_t has = __ballot(upto > slot);
-  if (has == 0) return 0;  // the same on every thread
-  const int at = __ffsll((unsigned long long)has) - 1;
-  uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)word, at);
-  int skip = slot - (__builtin_amdgcn_readlane(upto, at) - __popc(w));
-  for (; skip > 0; --skip) w &= w - 1;
-  expert = 32 * at + __ffs(w) - 1;
-  for (int i = tid; i < P; i += kThreads)
-    if (a.ids[i] == expert) s.pair[atomicAdd(&s.count, 1)] = (uint16_t)i;
+  int sum = 0;  // of this wave
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (i < each) sum += __popcll(__ballot(id[i] == (uint32_t)expert));
+  if (l == 0) s.count[wave] = sum;
   __syncthreads();
-  return s.count;
+  int n = 0, pos = 0;
+#pragma unroll
+  for (int u = 0; u < kWaves; ++u) {
+    if (u == wave) pos = n;
+    n += s.count[u];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (i < each) {
+      const uint64_t has = __ballot(id[i] == (uint32_t)expert);
+      if (id[i] == (uint32_t)expert)
+        s.list[pos + __popcll(has & (((uint64_t)1 << l) - 1))] = (uint16_t)(tid + kThreads * i);
+      pos += __popcll(has);
+    }
+  __syncthreads();
+  return n;
 }
 
 __device__ __forceinline__ v8bf expand(uint32_t codes, float scale) {
@@ -89,152 +130,296 @@ __device__ __forceinline__ v8bf expand(uint32_t codes, float scale) {
   const mx::v2bf p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
   return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
-
-// acc[r][c] (+)= rows 16r.. of the activations times 16-column group c of two 32-column
-// tiles (c / 2 the tile, c % 2 its half) over this wave's share of K: scale groups of 256 k,
-// wave, wave + kWaves, .... The weights are the first operand, so that result register i of
-// lane l is column 4 * (l / 16) + i of the group for row l % 16. Lane l supplies the 32
-// codes of column l % 16, k = 32 * (l / 16) .. +31 of a 128-k step, and the same k of its row.
-template <int NT>
-__device__ __forceinline__ void multiply(const Packed& p, const int (&tile)[2], const uint8_t* const (&row)[NT], int K,
-                                         int wave, mx::v4f (&acc)[NT][4]) {
-  const int l = threadIdx.x & 63, c = l & 15, g = l >> 4;
-  const uint8_t* unit[2];
-  const uint8_t* scale[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    unit[t] = p.units + (int64_t)tile[t] * p.KU * 1024;
-    scale[t] = p.scales + (int64_t)tile[t] * p.KG * 256;
-  }
-  const int lane = (g & 1) * 32 + c;  // of the unit's lanes, first half of its columns
-  for (int q = wave; q < p.KG; q += kWaves) {
-    u32x4 code[2][4];  // [step][column group]
-    uint32_t sc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = lane + 16 * (i & 1);
-      sc[i] = *reinterpret_cast<const uint32_t*>(scale[i >> 1] + (int64_t)q * 256 + 4 * at) >> (8 * (g >> 1));
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int u = 4 * q + 2 * s + (g >> 1);
-        const bool in = u < p.KU;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(unit[i >> 1] + (int64_t)(in ? u : p.KU - 1) * 1024 + 16 * at);
-        code[s][i] = in ? v : u32x4{0, 0, 0, 0};
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int k0 = min(256 * q + 128 * s + 32 * g, K - 32);  // past the end: the codes are zero
-      v8bf f[NT][4];
-#pragma unroll
-      for (int r = 0; r < NT; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[r][j] = *reinterpret_cast<const v8bf*>(row[r] + 2 * (int64_t)k0 + 16 * j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = __builtin_bit_cast(float, ((sc[i] >> (16 * s)) & 0xffu) << 23);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const v8bf w = expand(code[s][i][j], e);
-#pragma unroll
-          for (int r = 0; r < NT; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, f[r][j], acc[r][i], 0, 0, 0);
-        }
-      }
-    }
-  }
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const uint8_t* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, bytes, 0x00020000);
 }
 
-constexpr int kMaxNT = 4;
-struct Smem {
-  Rows rows;
-  mx::v4f red[kWaves][kMaxNT * 4][64];
+// A 32-column tile of a packed weight. Loads go through buffer resources over the tile's units
+// and scales: what lies past its K reads zeros, and makes no traffic.
+struct Tile {
+  __amdgpu_buffer_rsrc_t units, scales;
 };
-
-template <int NT>
-__device__ __forceinline__ void store_parts(const mx::v4f (&acc)[NT][4], int wave, Smem& sm) {
-  const int l = threadIdx.x & 63;
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < NT; ++r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sm.red[wave][r * 4 + i][l] = acc[r][i];
-  __syncthreads();
-}
-__device__ __forceinline__ mx::v4f sum_parts(const Smem& sm, int i, int l) {
-  mx::v4f v = sm.red[0][i][l];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) v = v + sm.red[w][i][l];
-  return v;
+__device__ __forceinline__ Tile tile_at(const Packed& p, int tile) {
+  return Tile{make_rsrc(p.units + (int64_t)tile * p.KU * 1024, p.KU * 1024),
+              make_rsrc(p.scales + (int64_t)tile * p.KG * 256, p.KG * 256)};
 }
 
-// 32 columns of gate and of up of one expert for 16 * NT of its pairs, and h.
-template <int NT>
-__device__ __forceinline__ void up_rows(const MoeArgs& a, const Packed& p, int tile, int first, int n, Smem& sm) {
-  const int tid = threadIdx.x, l = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint8_t* row[NT];
+// Lane l of a wave supplies column l % 16 of each of NC 16-column groups (group c: half c % 2
+// of tile c / 2), and row l % 16 of the activations, both for k = 32 * (l / 16) .. +31 of a
+// 128-k step. The weights are the matrix instruction's first operand: result register i of
+// lane l is column 4 * (l / 16) + i of the group for row l % 16.
+// A step's codes and the dwords of scales that it shares with its neighbour.
+template <int NC>
+struct Codes {
+  u32x4 w[NC];
+  uint32_t scale[NC];
+};
+// Group i is half i % 2 of tile i / 2; with `split` half `h` of tile i.
+template <int NC, bool SPLIT = false>
+__device__ __forceinline__ void load_codes(const Tile* t, int step, Codes<NC>& c, int h = 0) {
+  const int l = threadIdx.x & 63, g = l >> 4, lane = 32 * (g & 1) + (l & 15);
 #pragma unroll
-  for (int r = 0; r < NT; ++r) row[r] = a.x + (sm.rows.pair[min(first + 16 * r + (l & 15), n - 1)] / a.k) * a.ldx;
-  mx::v4f acc[NT][4];
+  for (int i = 0; i < NC; ++i)
+    c.scale[i] = __builtin_amdgcn_raw_buffer_load_b32(t[SPLIT ? i : i / 2].scales,
+                                                      256 * (step >> 1) + 4 * (lane + 16 * (SPLIT ? h : i & 1)), 0,
+                                                      kNonTemporal);
 #pragma unroll
-  for (int r = 0; r < NT; ++r)
+  for (int i = 0; i < NC; ++i)
+    c.w[i] = __builtin_amdgcn_raw_buffer_load_b128(
+        t[SPLIT ? i : i / 2].units, 2048 * step + 1024 * (g >> 1) + 16 * (lane + 16 * (SPLIT ? h : i & 1)), 0, kNonTemporal);
+}
+// acc[r][i] += rows 16 r .. times column group i over a step; f(r, pl, j): the lane's elements
+// 8 j .. 8 j + 7 of its row of tile r, of the row's PL parts whose sum it is.
+template <int NT, int PL, int NC, typename F>
+__device__ __forceinline__ void multiply(const Codes<NC>& c, int step, F f, mx::v4f (&acc)[NT][NC]) {
+  const int byte = 16 * (step & 1) + 8 * ((threadIdx.x & 63) >> 5);  // the lane's unit of the step's two
+  float e[NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[r][i] = mx::v4f{0.f, 0.f, 0.f, 0.f};
-  const int tiles[2] = {tile, a.I / 32 + tile};
-  multiply<NT>(p, tiles, row, a.H, wave, acc);
-  store_parts<NT>(acc, wave, sm);
-  for (int i = tid; i < NT * 2 * 64; i += kThreads) {
-    const int r = i >> 7, half = (i >> 6) & 1;
-    const int at = first + 16 * r + (l & 15);
-    const mx::v4f g = sum_parts(sm, 4 * r + half, l), u = sum_parts(sm, 4 * r + 2 + half, l);
-    float h[4];
+  for (int i = 0; i < NC; ++i) {
+    uint32_t sc = c.scale[i];
+    asm volatile("" : "+v"(sc));  // else the shift follows its load, which it would wait for, a step before its use
+    e[i] = __builtin_bit_cast(float, (sc >> byte & 0xffu) << 23);
+  }
+  // A quarter's operands are asked for before the products of the quarter in front of it.
+  v8bf x[2][NT][PL];
+  auto get = [&](int j) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = g[e] / (1.0f + expf(-g[e])) * u[e];
-    if (at < n)
-      *reinterpret_cast<u32x2*>(a.h + ((int64_t)sm.rows.pair[at] * a.I + 32 * tile + 16 * half + 4 * (l >> 4)) * 2) =
-          u32x2{mx::pack_bf16x2(h[0], h[1]), mx::pack_bf16x2(h[2], h[3])};
+    for (int r = 0; r < NT; ++r)
+#pragma unroll
+      for (int pl = 0; pl < PL; ++pl) x[j & 1][r][pl] = f(r, pl, j);
+  };
+  get(0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j < 3) get(j + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const v8bf w = expand(c.w[i][j], e[i]);
+#pragma unroll
+      for (int pl = 0; pl < PL; ++pl)
+#pragma unroll
+        for (int r = 0; r < NT; ++r)
+          acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[j & 1][r][pl], acc[r][i], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// 64 columns of the down product of one expert for 16 * NT of its pairs.
-template <int NT>
-__device__ __forceinline__ void down_rows(const MoeArgs& a, const Packed& p, int block, int first, int n, Smem& sm) {
-  const int tid = threadIdx.x, l = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint8_t* row[NT];
-#pragma unroll
-  for (int r = 0; r < NT; ++r) row[r] = a.h + (int64_t)sm.rows.pair[min(first + 16 * r + (l & 15), n - 1)] * a.I * 2;
-  mx::v4f acc[NT][4];
+template <int NT, int NC>
+__device__ __forceinline__ void clear(mx::v4f (&acc)[NT][NC]) {
 #pragma unroll
   for (int r = 0; r < NT; ++r)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[r][i] = mx::v4f{0.f, 0.f, 0.f, 0.f};
-  const int tiles[2] = {2 * block, min(2 * block + 1, a.H / 32 - 1)};
-  multiply<NT>(p, tiles, row, a.I, wave, acc);
-  store_parts<NT>(acc, wave, sm);
-  for (int i = tid; i < NT * 4 * 64; i += kThreads) {
-    const int r = i >> 8, c = (i >> 6) & 3;
-    const int at = first + 16 * r + (l & 15), col = 64 * block + 16 * c + 4 * (l >> 4);
-    if (at < n && col < a.H)
-      *reinterpret_cast<mx::v4f*>(a.part + (int64_t)sm.rows.pair[at] * a.H + col) = sum_parts(sm, 4 * r + c, l);
+    for (int i = 0; i < NC; ++i) acc[r][i] = mx::v4f{0.f, 0.f, 0.f, 0.f};
+}
+
+// h of a pair is kept as two bf16 parts, the value's rounding and the rest's (within 2^-17 of it
+// together): one part alone would put an error into y as large as y's own rounding. The second
+// part costs a matrix instruction more, where the bytes of the weights set the time.
+__device__ __forceinline__ const uint8_t* h_row(const MoeArgs& a, int part, int pair) {
+  return a.h + ((int64_t)part * a.T * a.k + pair) * a.I * 2;
+}
+// Four columns of h of a pair, times the pair's weight.
+__device__ __forceinline__ void store_h(const MoeArgs& a, int pair, int col, const mx::v4f& g, const mx::v4f& u) {
+  const float w = a.weights[pair];
+  float h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = g[e] / (1.0f + expf(-g[e])) * u[e] * w;
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    const u32x2 v = {mx::pack_bf16x2(h[0], h[1]), mx::pack_bf16x2(h[2], h[3])};
+    *reinterpret_cast<u32x2*>(const_cast<uint8_t*>(h_row(a, part, pair)) + 2 * col) = v;
+    h[0] -= __builtin_bit_cast(float, v.x << 16);
+    h[1] -= __builtin_bit_cast(float, v.x & 0xffff0000u);
+    h[2] -= __builtin_bit_cast(float, v.y << 16);
+    h[3] -= __builtin_bit_cast(float, v.y & 0xffff0000u);
   }
 }
 
-template <bool UP>
-__global__ __launch_bounds__(kThreads) void experts_kernel(MoeArgs a) {
-  __shared__ __align__(16) Smem sm;
+// ---------------------------------------------------------------------------
+// Gate and up, few rows to an expert: 32 columns of each to a workgroup, K split over its waves
+// ---------------------------------------------------------------------------
+// Steps of 128 k: wave, wave + kWaves, .... Activations come straight from L2. No step is fetched
+// ahead: the registers that it would take leave room for fewer waves, which hide more (64
+// tokens through 64 experts of H 7168, I 2048: no step ahead 177 us, one 184, three 200).
+struct FewSmem {
+  Rows rows;
+  mx::v4f red[kWaves][4][64];
+};
+__global__ __launch_bounds__(kThreads) void few_kernel(MoeArgs a) {
+  __shared__ __align__(16) FewSmem sm;
+  const int tid = threadIdx.x, l = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), b = blockIdx.x;
   int expert = 0;
   const int n = find_rows(a, blockIdx.y, sm.rows, expert);
   if (n == 0) return;
-  expert = __builtin_amdgcn_readfirstlane(expert);
-  const Packed p = UP ? packed(a.w13 + expert * a.stride13, 2 * a.I, a.H) : packed(a.w2 + expert * a.stride2, a.H, a.I);
-  for (int first = 0; first < n; first += 16 * kMaxNT) {
-    const int left = n - first;
-    if (left <= 16)
-      UP ? up_rows<1>(a, p, blockIdx.x, first, n, sm) : down_rows<1>(a, p, blockIdx.x, first, n, sm);
-    else if (left <= 32)
-      UP ? up_rows<2>(a, p, blockIdx.x, first, n, sm) : down_rows<2>(a, p, blockIdx.x, first, n, sm);
-    else
-      UP ? up_rows<4>(a, p, blockIdx.x, first, n, sm) : down_rows<4>(a, p, blockIdx.x, first, n, sm);
+  const Packed p = packed(a.w13 + __builtin_amdgcn_readfirstlane(expert) * a.stride13, 2 * a.I, a.H);
+  const Tile t[2] = {tile_at(p, b), tile_at(p, a.I / 32 + b)};
+  for (int first = 0; first < n; first += 16) {
+    const int at = first + (l & 15), pair = sm.rows.list[min(at, n - 1)];
+    const uint8_t* row = a.x + pair / a.k * a.ldx;
+    mx::v4f acc[1][4];
+    clear(acc);
+    const int steps = (a.H + 127) / 128, g = l >> 4;
+#pragma unroll 1
+    for (int s = wave; s < steps; s += kWaves) {
+      Codes<4> code;
+      v8bf x[4];
+      load_codes<4>(t, s, code);
+      const int k = min(128 * s + 32 * g, a.H - 32);  // past the end: the codes are zero
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const v8bf*>(row + 2 * (int64_t)k + 16 * j);
+      multiply<1, 1, 4>(code, s, [&](int, int, int j) { return x[j]; }, acc);
+    }
+    __syncthreads();  // the last rows' sums
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sm.red[wave][i][l] = acc[0][i];
     __syncthreads();
+    if (wave < 2) {  // a half of the columns each
+      mx::v4f g = sm.red[0][wave][l], u = sm.red[0][2 + wave][l];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) {
+        g = g + sm.red[w][wave][l];
+        u = u + sm.red[w][2 + wave][l];
+      }
+      if (at < n) store_h(a, pair, 32 * b + 16 * wave + 4 * (l >> 4), g, u);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// More rows to an expert, and the down product: 64 columns to a wave, activations through LDS
+// ---------------------------------------------------------------------------
+// A 128-k step of up to 64 rows lies in LDS as 16 pieces of 16 bytes to a row, piece p of row r
+// at p ^ (r % 16): the operand reads (one piece of 16 rows) and the writes (a row's pieces) hit
+// distinct banks. Two buffers, one barrier to a step. PL: the rows' parts.
+template <int MAXNT, int PL>
+struct ManySmem {
+  Rows rows;
+  u32x4 x[2][PL][16 * MAXNT][16];
+};
+template <int NT, int PL, int NC>
+struct ManyStep {
+  Codes<NC> code;
+  u32x4 x[PL][NT];
+};
+// A wave's columns: 8 NC of gate and the same of up, or 16 NC of the down product. A wave past the
+// last ones repeats them and stores nothing: it still fetches its share of rows.
+template <bool UP, int NC>
+struct Columns {
+  Tile t[2];
+  int unit, units, half;
+  __device__ __forceinline__ Columns(const MoeArgs& a, int expert) {
+    const Packed p = UP ? packed(a.w13 + expert * a.stride13, 2 * a.I, a.H) : packed(a.w2 + expert * a.stride2, a.H, a.I);
+    unit = kWaves * blockIdx.x + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    units = UP ? a.I / (8 * NC) : (a.H + 16 * NC - 1) / (16 * NC);
+    const int u = min(unit, units - 1), t0 = UP ? u * NC / 4 : u * NC / 2;
+    half = u & 1;
+    t[0] = tile_at(p, t0);
+    t[1] = tile_at(p, UP ? a.I / 32 + t0 : min(t0 + 1, a.H / 32 - 1));
+  }
+  __device__ __forceinline__ void load(int step, Codes<NC>& c) const { load_codes<NC, UP && NC == 2>(t, step, c, half); }
+};
+template <bool UP, int NT, int NC, typename SMEM>
+__device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC>& o, int first, int n, SMEM& sm,
+                                          const Codes<NC> (&begin)[2]) {
+  constexpr int PL = UP ? 1 : 2;
+  const int tid = threadIdx.x, l = tid & 63, c = l & 15, g = l >> 4;
+  const int K = UP ? a.H : a.I;
+  const int piece = tid & 15;
+  const uint8_t* row[PL][NT];  // of the rows that this thread fetches a piece of
+#pragma unroll
+  for (int r = 0; r < NT; ++r) {
+    const int pair = sm.rows.list[min(first + 16 * r + (tid >> 4), n - 1)];
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl) row[pl][r] = (UP ? a.x + pair / a.k * a.ldx : h_row(a, pl, pair)) + 16 * piece;
+  }
+  mx::v4f acc[NT][NC];
+  clear(acc);
+  const int steps = (K + 127) / 128;
+  auto load = [&](int s, ManyStep<NT, PL, NC>& v) {
+    if (s >= 2) o.load(s, v.code);
+    const int64_t at = 128 * s + 8 * piece < K ? 256 * (int64_t)s : -16 * (int64_t)piece;  // past K: the row's start
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl)
+#pragma unroll
+      for (int r = 0; r < NT; ++r) v.x[pl][r] = *reinterpret_cast<const u32x4*>(row[pl][r] + at);
+  };
+  auto put = [&](const ManyStep<NT, PL, NC>& v, int buf) {
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl)
+#pragma unroll
+      for (int r = 0; r < NT; ++r) sm.x[buf][pl][16 * r + (tid >> 4)][piece ^ (tid >> 4)] = v.x[pl][r];
+  };
+  ManyStep<NT, PL, NC> v[2];
+  load(0, v[0]);
+  load(1, v[1]);
+  v[0].code = begin[0];
+  v[1].code = begin[1];
+  put(v[0], 0);
+  for (int s = 0; s < steps; s += 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      __syncthreads();
+      put(v[1 - i], 1 - i);
+      const Codes<NC> code = v[i].code;
+      load(s + i + 2, v[i]);
+      __builtin_amdgcn_sched_barrier(0);  // keeps the loads ahead of the products
+      if (s + i < steps)
+        multiply<NT, PL, NC>(code, i, [&](int r, int pl, int j) {
+          return __builtin_bit_cast(v8bf, sm.x[i][pl][16 * r + c][(4 * g + j) ^ c]);
+        }, acc);
+    }
+  }
+  if (o.unit >= o.units) return;  // whole waves; the caller's barrier is after the loop
+#pragma unroll
+  for (int r = 0; r < NT; ++r) {
+    const int at = first + 16 * r + c;
+    if (at >= n) continue;
+    const int pair = sm.rows.list[at];
+    if constexpr (UP) {
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) store_h(a, pair, 8 * NC * o.unit + 16 * i + 4 * g, acc[r][i], acc[r][NC / 2 + i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int col = 16 * NC * o.unit + 16 * i + 4 * g;
+        if (col < a.H) *reinterpret_cast<mx::v4f*>(a.part + (int64_t)pair * a.H + col) = acc[r][i];
+      }
+    }
+  }
+}
+
+// MAXNT row tiles at most go together.
+template <bool UP, int MAXNT, int NC>
+__global__ __launch_bounds__(kThreads) void many_kernel(MoeArgs a) {
+  __shared__ __align__(16) ManySmem<MAXNT, UP ? 1 : 2> sm;
+  int expert = blockIdx.y;
+  Codes<NC> begin[2];
+  auto start = [&]() {
+    const Columns<UP, NC> o(a, __builtin_amdgcn_readfirstlane(expert));
+    o.load(0, begin[0]);
+    o.load(1, begin[1]);
+  };
+  // The weight is asked for before the rows are known, where the expert is.
+  const bool direct = slot_is_expert(a);
+  if (direct) start();
+  const int n = find_rows(a, blockIdx.y, sm.rows, expert);
+  if (n == 0) return;
+  if (!direct) start();
+  const Columns<UP, NC> o(a, __builtin_amdgcn_readfirstlane(expert));
+  for (int first = 0; first < n; first += 16 * MAXNT) {
+    const int left = n - first;
+    if (MAXNT == 1 || left <= 16)
+      many_rows<UP, 1, NC>(a, o, first, n, sm, begin);
+    else if (left <= 32)
+      many_rows<UP, MAXNT == 1 ? 1 : 2, NC>(a, o, first, n, sm, begin);
+    else if (left <= 48)
+      many_rows<UP, MAXNT == 1 ? 1 : 3, NC>(a, o, first, n, sm, begin);
+    else
+      many_rows<UP, MAXNT, NC>(a, o, first, n, sm, begin);
+    __syncthreads();
+    if (left > 16 * MAXNT) start();
   }
 }
 
@@ -243,14 +428,137 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
   const int t = blockIdx.y, col = 4 * (blockIdx.x * 256 + threadIdx.x);
   if (col >= a.H) return;
   mx::v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int j = 0; j < a.k; ++j) {
     const int64_t p = (int64_t)t * a.k + j;
-    if ((uint32_t)a.ids[p] < (uint32_t)a.E) {
-      const mx::v4f q = *reinterpret_cast<const mx::v4f*>(a.part + p * a.H + col);
-      v = v + a.weights[p] * q;
-    }
+    if ((uint32_t)a.ids[p] < (uint32_t)a.E) v = v + *reinterpret_cast<const mx::v4f*>(a.part + p * a.H + col);
   }
   *reinterpret_cast<u32x2*>(a.y + t * a.ldy + 2 * col) = u32x2{mx::pack_bf16x2(v[0], v[1]), mx::pack_bf16x2(v[2], v[3])};
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the down product over all their experts, 32 columns to a workgroup
+// ---------------------------------------------------------------------------
+// The rows are the tokens, so that the sum over a token's experts is the matrix instruction's
+// own: no partial products in memory, no launch to add them. The work is a list of (expert,
+// 128 k), taken in turn by the waves; h of all pairs lies in LDS, piece p (8 k) of a row of
+// token t at p ^ t, which spreads a piece of the tokens over distinct banks. A token without the
+// expert has a row of zeros.
+constexpr int kTokens = 16, kTokenPairs = 64;
+constexpr int kTokenPieces = 2048;  // of 8 k: all pairs' I, each rounded up to 128
+constexpr int kTokenWaves = 16;
+struct TokenSmem {
+  u32x4 h[2][kTokenPieces];
+  u32x4 zero;
+  int expert[kTokenPairs];             // of a slot
+  int16_t pair[kTokenPairs][kTokens];  // of a slot's token, -1 without one
+  mx::v4f red[kTokenWaves][2][64];
+};
+// Slots are the distinct (expert, turn) in the order of their first pairs; a pair's turn is how
+// often its token has its expert before. Lane p of every wave has pair p. Returns their number.
+__device__ __forceinline__ int find_slots(const MoeArgs& a, TokenSmem& s) {
+  const int tid = threadIdx.x, l = tid & 63, P = a.T * a.k;
+  const int id = l < P ? a.ids[l] : -1, token = l / a.k;
+  const bool there = (uint32_t)id < (uint32_t)a.E;
+  for (int i = tid; i < kTokenPairs * kTokens / 2; i += 64 * kTokenWaves) reinterpret_cast<uint32_t*>(s.pair)[i] = ~0u;
+  int lead = l;  // one token: every pair is a slot of its own
+  if (a.T > 1) {
+    int turn = 0;
+    for (int i = 0; i < P; ++i) turn += i < l && __builtin_amdgcn_readlane(id, i) == id && i / a.k == token;
+    for (int i = P - 1; i >= 0; --i)
+      if (__builtin_amdgcn_readlane(id, i) == id && __builtin_amdgcn_readlane(turn, i) == turn && i < l) lead = i;
+  }
+  const uint64_t leads = __ballot(there && lead == l);
+  const int slot = __popcll(leads & (((uint64_t)1 << lead) - 1));
+  __syncthreads();
+  if (tid < 64 && there) {
+    if (lead == l) s.expert[slot] = id;
+    s.pair[slot][token] = (int16_t)l;
+  }
+  __syncthreads();
+  return __popcll(leads);
+}
+__global__ __launch_bounds__(64 * kTokenWaves) void tokens_kernel(MoeArgs a) {
+  __shared__ __align__(16) TokenSmem sm;
+  const int tid = threadIdx.x, l = tid & 63, c = l & 15, g = l >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int P = a.T * a.k, steps = (a.I + 127) / 128, pieces = 16 * steps;  // of a row
+  // Everyone's h is asked for before the slots are known.
+  constexpr int kEach = kTokenPieces / (64 * kTokenWaves);
+  u32x4 held[2][kEach];
+  int at[kEach];
+  {
+    int pair = tid / pieces, p = tid - pair * pieces;
+    const int by = 64 * kTokenWaves / pieces, rest = 64 * kTokenWaves - by * pieces;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      at[i] = pair < P ? pair * pieces + (p ^ (pair / a.k)) : -1;
+#pragma unroll
+      for (int pl = 0; pl < 2; ++pl) {
+        held[pl][i] = u32x4{0, 0, 0, 0};
+        if (pair < P && 8 * p < a.I) held[pl][i] = *reinterpret_cast<const u32x4*>(h_row(a, pl, pair) + 16 * p);
+      }
+      pair += by;
+      p += rest;
+      if (p >= pieces) {
+        p -= pieces;
+        ++pair;
+      }
+    }
+  }
+  if (tid == 0) sm.zero = u32x4{0, 0, 0, 0};
+  const int slots = find_slots(a, sm);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+#pragma unroll
+    for (int pl = 0; pl < 2; ++pl)
+      if (at[i] >= 0) sm.h[pl][at[i]] = held[pl][i];
+  __syncthreads();
+  mx::v4f acc[1][2];
+  clear(acc);
+  int slot = wave / steps, s = wave - slot * steps;
+  const int by = kTokenWaves / steps, rest = kTokenWaves - by * steps;
+#pragma unroll 1
+  while (slot < slots) {
+    const Packed p = packed(a.w2 + __builtin_amdgcn_readfirstlane(sm.expert[slot]) * a.stride2, a.H, a.I);
+    const Tile t[1] = {tile_at(p, blockIdx.x)};
+    Codes<2> code;
+    load_codes<2>(t, s, code);
+    const int pair = sm.pair[slot][c];
+    multiply<1, 2, 2>(code, s, [&](int, int pl, int j) {
+      const u32x4* x = pair >= 0 ? &sm.h[pl][pair * pieces + ((16 * s + 4 * g + j) ^ c)] : &sm.zero;
+      return __builtin_bit_cast(v8bf, *x);
+    }, acc);
+    slot += by;
+    s += rest;
+    if (s >= steps) {
+      s -= steps;
+      ++slot;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) sm.red[wave][i][l] = acc[0][i];
+  __syncthreads();
+  if (wave >= 2 || c >= a.T) return;
+  mx::v4f y = sm.red[0][wave][l];
+#pragma unroll
+  for (int w = 1; w < kTokenWaves; ++w) y = y + sm.red[w][wave][l];
+  *reinterpret_cast<u32x2*>(a.y + c * a.ldy + 2 * (32 * (int)blockIdx.x + 16 * wave + 4 * g)) =
+      u32x2{mx::pack_bf16x2(y[0], y[1]), mx::pack_bf16x2(y[2], y[3])};
+}
+
+// 64 columns to a wave, or 32 where that would leave the chip short of workgroups (down product
+// of 37 tokens and 24 experts, I 1056, H 2112, 216 or 408 workgroups: 11.8 and 11.1 us; of 64
+// tokens and 64 experts, I 2048, H 7168, 1792 or 3584: 94 and 95).
+template <bool UP, int MAXNT>
+hipError_t launch_many(MoeArgs& a, unsigned slots, hipStream_t st) {
+  void* args[] = {&a};
+  const unsigned units = (unsigned)mxh::cdiv(UP ? a.I : a.H, UP ? 32 * kWaves : 64 * kWaves);
+  if (units * slots >= 600)
+    return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 4>, dim3(units, slots), dim3(kThreads), args, 0, st);
+  return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 2>,
+                         dim3((unsigned)mxh::cdiv(UP ? a.I : a.H, UP ? 16 * kWaves : 32 * kWaves), slots), dim3(kThreads),
+                         args, 0, st);
 }
 
 bool shape_ok(int64_t T, int64_t k, int64_t H, int64_t I) {
@@ -258,7 +566,7 @@ bool shape_ok(int64_t T, int64_t k, int64_t H, int64_t I) {
   return T >= 1 && k >= 1 && T <= MXFP4_MOE_MAX_PAIRS && k <= MXFP4_MOE_MAX_PAIRS && T * k <= MXFP4_MOE_MAX_PAIRS &&
          H >= 32 && H <= kMaxRow && H % 32 == 0 && I >= 32 && I <= kMaxRow && I % 32 == 0;
 }
-size_t h_bytes(int64_t T, int64_t k, int64_t I) { return (size_t)(T * k * I * 2 + 255) / 256 * 256; }
+size_t h_bytes(int64_t T, int64_t k, int64_t I) { return (size_t)(T * k * I * 4 + 255) / 256 * 256; }  // two parts
 
 }  // namespace
 
@@ -289,12 +597,16 @@ extern "C" int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const f
             (float*)((uint8_t*)workspace + h_bytes(T, k, I)), (int)T, (int)k, (int)E, (int)H, (int)I};
   void* args[] = {&a};
   const hipStream_t st = (hipStream_t)stream;
-  const unsigned slots = (unsigned)(T * k < E ? T * k : E);
-  hipError_t e = hipLaunchKernel((const void*)experts_kernel<true>, dim3((unsigned)(I / 32), slots), dim3(kThreads), args,
-                                 0, st);
+  const int64_t P = T * k;
+  const bool many = P > 10 * E;  // rows to an expert
+  const unsigned slots = (unsigned)(P <= 64 || P < E ? P : E), tiles = (unsigned)(I / 32);
+  hipError_t e = many ? launch_many<true, 4>(a, slots, st)
+                      : hipLaunchKernel((const void*)few_kernel, dim3(tiles, slots), dim3(kThreads), args, 0, st);
   if (e != hipSuccess) return MXFP4_ERR_HIP;
-  e = hipLaunchKernel((const void*)experts_kernel<false>, dim3((unsigned)mxh::cdiv(H, 64), slots), dim3(kThreads), args,
-                      0, st);
+  if (T <= kTokens && P <= kTokenPairs && P * mxh::cdiv(I, 128) * 16 <= kTokenPieces)
+    return mxh::launch_status(hipLaunchKernel((const void*)tokens_kernel, dim3((unsigned)(H / 32)),
+                                              dim3(64 * kTokenWaves), args, 0, st));
+  e = many ? launch_many<false, 4>(a, slots, st) : launch_many<false, 1>(a, slots, st);
   if (e != hipSuccess) return MXFP4_ERR_HIP;
   return mxh::launch_status(hipLaunchKernel((const void*)combine_kernel, dim3((unsigned)mxh::cdiv(H, 1024), (unsigned)T),
                                             dim3(256), args, 0, st));

@@ -1,11 +1,13 @@
 // moe_route: the k experts of each token and their weights, from the router's logits.
 //
-// One wave to a row. Lane l holds the logits l, l + 64, ...; without a bias the rank is
-// the logit itself, as an integer that orders like it (32 bits), with one it is score +
-// bias in float64 (64 bits): a last bit of a rounded score would change choices that lie
-// close together, and a row has too few values for the float64 work to show. k rounds take
-// the largest (rank, lowest index) over the wave; a lane looks for its next candidate only
-// after one of its own was taken.
+// One wave to a row; lane l holds the S neighbouring logits from l * S on. Without a bias the
+// rank is the logit itself, as an integer that orders like it (32 bits), with one it is score +
+// bias in float64 (64 bits): a last bit of a rounded score would change choices that lie close
+// together, and a row has too few values for the float64 work to show. k rounds take the
+// largest rank over the wave; equal ranks go to the lowest lane, and a lane's own candidate is
+// its first, so that the lowest index wins without being compared. Reductions run over DPP
+// moves, a few cycles each; a shuffle through LDS takes over 100, and a row needs about 60 in
+// turn. TIMES
 #include "host_common.hpp"
 
 #pragma clang fp contract(off)
@@ -41,49 +43,85 @@ __device__ __forceinline__ uint64_t order64(double v) {
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s, 64));
-  return v;
+// v of the lane that the step's move takes it from; `none` for lanes without one. After the
+// steps 0 to 5, each combined with the lane's own, lane 63 has all lanes' values.
+template <int STEP>
+__device__ __forceinline__ uint32_t moved(uint32_t v, uint32_t none) {
+  constexpr int kCtrl[6] = {0x111, 0x112, 0x114, 0x118, 0x142, 0x143};  // row_shr 1, 2, 4, 8, row_bcast 15, 31
+  constexpr int kRowMask[6] = {0xf, 0xf, 0xf, 0xf, 0xa, 0xc};
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, kCtrl[STEP], kRowMask[STEP], 0xf, false);
 }
+template <int STEP = 0>
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  if constexpr (STEP == 6) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  } else {
+    const uint32_t o = moved<STEP>(v, 0);
+    return wave_max<STEP + 1>(v > o ? v : o);
+  }
+}
+template <int STEP = 0>
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) v = v + __shfl_xor(v, s, 64);
-  return v;
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  if constexpr (STEP == 6) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  } else {
+    const uint64_t o = (uint64_t)moved<STEP>((uint32_t)(b >> 32), 0) << 32 | moved<STEP>((uint32_t)b, 0);
+    return wave_sum<STEP + 1>(v + __builtin_bit_cast(double, o));
+  }
+}
+// The value of the largest key (0 if all are), the same on every lane.
+__device__ __forceinline__ uint32_t largest(uint32_t k) { return wave_max(k); }
+__device__ __forceinline__ uint64_t largest(uint64_t k) {
+  const uint32_t hi = wave_max((uint32_t)(k >> 32));
+  const uint32_t lo = wave_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (uint64_t)hi << 32 | lo;
 }
 
 constexpr int kRows = 4;  // rows (waves) to a workgroup
 
-// S logits to a lane (E <= 64 S).
+// E <= 64 S.
 template <int DT, int S, bool BIAS>
 __global__ __launch_bounds__(64 * kRows) void route_kernel(RouteArgs a) {
   typedef typename std::conditional<BIAS, uint64_t, uint32_t>::type Key;
   const int l = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * kRows + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (row >= a.T) return;  // whole waves, and there is no barrier
   const int64_t base = row * a.ldl;
-  float v[S];
+  float v[S], bias[S];
 #pragma unroll
-  for (int i = 0; i < S; ++i) v[i] = l + 64 * i < a.E ? logit_at<DT>(a.logits, base + l + 64 * i) : -__builtin_inff();
-  float top = -__builtin_inff();
+  for (int i = 0; i < S; ++i) {
+    const int e = S * l + i;
+    v[i] = e < a.E ? logit_at<DT>(a.logits, base + e) : -__builtin_inff();
+    if constexpr (BIAS) bias[i] = e < a.E ? a.bias[e] : 0.0f;
+  }
+  uint32_t order[S], best32 = 0;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     bad |= !(v[i] < __builtin_inff());  // NaN or +Inf
-    top = fmaxf(top, v[i]);
+    order[i] = v[i] > -__builtin_inff() ? order32(v[i]) : 0;
+    best32 = best32 > order[i] ? best32 : order[i];
   }
-  top = wave_max(top);
+  // The row's largest logit (any value for a row without one).
+  const uint32_t top32 = largest(best32);
+  const double top = (double)__builtin_bit_cast(float, top32 & 0x80000000u ? top32 & 0x7fffffffu : ~top32);
   // The softmax's sum over the row is needed for its scores as ranks or as weights.
-  double total = 0.0;
+  double total = 0.0, scores[S];
   const bool sums = !a.sigmoid && (BIAS || !a.renormalize);
   if (sums) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) total = total + (v[i] > -__builtin_inff() ? exp((double)v[i] - (double)top) : 0.0);
+    for (int i = 0; i < S; ++i) {
+      scores[i] = v[i] > -__builtin_inff() ? exp((double)v[i] - top) : 0.0;
+      total = total + scores[i];
+    }
     total = wave_sum(total);
   }
   auto score = [&](float x) {
     if (a.sigmoid) return 1.0 / (1.0 + exp(-(double)x));
-    const double p = exp((double)x - (double)top);
+    const double p = exp((double)x - top);
     return sums ? p / total : p;
   };
   Key key[S];  // 0: cannot be chosen (the order of every real value is larger)
@@ -91,19 +129,19 @@ __global__ __launch_bounds__(64 * kRows) void route_kernel(RouteArgs a) {
   for (int i = 0; i < S; ++i) {
     if constexpr (BIAS) {
       key[i] = 0;
-      if (v[i] > -__builtin_inff()) {
-        const double r = score(v[i]) + (double)a.bias[l + 64 * i];
+      if (order[i] != 0) {
+        const double r = (a.sigmoid ? score(v[i]) : scores[i] / total) + (double)bias[i];
         bad |= !(r < __builtin_inf());
         key[i] = r > -__builtin_inf() ? order64(r) : 0;
       }
     } else {
-      key[i] = v[i] > -__builtin_inff() ? order32(v[i]) : 0;
+      key[i] = order[i];
     }
   }
   if (__ballot(bad)) {
-    for (int j = l; j < a.k; j += 64) {
-      a.ids[row * a.k + j] = j;
-      a.weights[row * a.k + j] = __builtin_nanf("");
+    if (l < a.k) {
+      a.ids[row * a.k + l] = l;
+      a.weights[row * a.k + l] = __builtin_nanf("");
     }
     return;
   }
@@ -113,43 +151,33 @@ __global__ __launch_bounds__(64 * kRows) void route_kernel(RouteArgs a) {
   float val;
   auto candidate = [&]() {
     best = key[0];
-    at = l;
+    at = 0;
     val = v[0];
 #pragma unroll
     for (int i = 1; i < S; ++i)
       if (key[i] > best) {
         best = key[i];
-        at = l + 64 * i;
+        at = i;
         val = v[i];
       }
   };
   candidate();
-  int id = -1;      // lane j keeps choice j
+  int id = -1;  // lane j keeps choice j
   float chosen = 0.0f;
   for (int j = 0; j < a.k; ++j) {
-    Key b = best;
-    int e = at;
-    float x = val;
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) {
-      const Key ob = __shfl_xor(b, s, 64);
-      const int oe = __shfl_xor(e, s, 64);
-      const float ox = __shfl_xor(x, s, 64);
-      if (ob > b || (ob == b && oe < e)) {
-        b = ob;
-        e = oe;
-        x = ox;
-      }
-    }
+    const Key b = largest(best);
     if (b == 0) break;  // nothing left, the same on every lane
+    const int lane = __ffsll((unsigned long long)__ballot(best == b)) - 1;
+    const int i0 = __builtin_amdgcn_readlane(at, lane);
+    const float x = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, val), lane));
     if (l == j) {
-      id = e;
+      id = S * lane + i0;
       chosen = x;
     }
-    if (at == e) {
+    if (l == lane) {
 #pragma unroll
       for (int i = 0; i < S; ++i)
-        if (l + 64 * i == e) key[i] = 0;
+        if (i == i0) key[i] = 0;
       candidate();
     }
   }
@@ -173,7 +201,9 @@ hipError_t launch_bias(RouteArgs& a, hipStream_t st) {
 template <int DT>
 hipError_t launch_size(RouteArgs& a, hipStream_t st) {
   if (a.E <= 64) return launch_bias<DT, 1>(a, st);
+  if (a.E <= 128) return launch_bias<DT, 2>(a, st);
   if (a.E <= 256) return launch_bias<DT, 4>(a, st);
+  if (a.E <= 512) return launch_bias<DT, 8>(a, st);
   return launch_bias<DT, 16>(a, st);
 }
 
