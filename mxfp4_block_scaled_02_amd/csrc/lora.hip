@@ -259,13 +259,14 @@ struct Row16 {
   static __device__ __forceinline__ int column(int g, int j) {
     return 4 * kPer * (4 * j / kPer) + kPer * g + 4 * j % kPer;
   }
-  // `row`: the wave's first column; `left` of its columns are there.
+  // `row`: the wave's first column; `left` of its columns are there (FULL: all).
+  template <bool FULL>
   static __device__ __forceinline__ void load(const uint8_t* row, int g, int left, uint32_t (&w)[kWords]) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int n = 4 * kPer * i + kPer * g;
       const uint8_t* at = row + n * kSize;
-      if (n + kPer <= left) {
+      if constexpr (FULL) {
         u32x4 p;
         if constexpr (kSize == 4)
           p = *reinterpret_cast<const u32x4_at4*>(at);
@@ -305,6 +306,7 @@ struct Row16 {
       }
     }
   }
+  template <bool FULL>
   static __device__ __forceinline__ void store(uint8_t* row, int g, int left, const float (&v)[16]) {
     uint32_t w[kWords];
 #pragma unroll
@@ -323,7 +325,7 @@ struct Row16 {
     for (int i = 0; i < kPieces; ++i) {
       const int n = 4 * kPer * i + kPer * g;
       uint8_t* at = row + n * kSize;
-      if (n + kPer <= left) {
+      if constexpr (FULL) {
         const u32x4 p = {w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
         if constexpr (kSize == 4)
           *reinterpret_cast<u32x4_at4*>(at) = p;
@@ -353,15 +355,80 @@ constexpr int expand_tiles() {  // row tiles that go together: their rows of y a
   return YT == MXFP4_TYPE_F32 || RS == 4 ? 2 : 4;
 }
 template <int DT, int YT, int RS>
-__global__ __launch_bounds__(kExpandThreads, RS == 4 ? 2 : 3) void expand_kernel(LoraArgs a) {
+struct ExpandSmem {
+  // Ranks of a row in pieces of 8, one row 16 bytes longer than its ranks.
+  typename Half<DT>::V u[YT == MXFP4_TYPE_F32 ? 3 : 2][16 * expand_tiles<YT, RS>()][4 * RS + 1];
+  float back[16 * expand_tiles<YT, RS>()];  // undoes the power of two
+};
+// 64 columns, from n0 on, of a unit's rows. FULL: y has all of them.
+template <int DT, int YT, int RS>
+struct Columns {
   typedef typename Half<DT>::V V;
   typedef Row16<YT> Y;
+  static constexpr int kPieces = YT == MXFP4_TYPE_F32 ? 3 : 2, kTiles = expand_tiles<YT, RS>();
+  V bv[4][RS];
+  uint8_t* at[kTiles];
+  uint32_t held[kTiles][Y::kWords];
+
+  template <bool FULL>
+  __device__ __forceinline__ void load(const LoraArgs& a, int adapter, int row0, int n0, int order, int first, int count) {
+    const int l = threadIdx.x & 63, c = l & 15, g = l >> 4;
+    // Row c of the operand of column group j is column Y::column(c / 4, j) + c % 4: result register e of
+    // group j of lane l is column Y::column(g, j) + e. Past R the pieces are zeros, and B's are any.
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = min(n0 + Y::column(c >> 2, j) + (c & 3), a.N - 1);
+      const uint8_t* br = a.b + ((int64_t)adapter * a.N + n) * a.R * 2;
+#pragma unroll
+      for (int s = 0; s < RS; ++s) {
+        const int rank = 32 * s + 8 * g;
+        bv[j][s] = *reinterpret_cast<const V*>(br + (rank < a.R ? 2 * rank : 0));
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) {
+      const int row = row0 + __shfl(order, first + min(16 * m + c, count - 1), 64);
+      at[m] = a.y + ((int64_t)row * a.ldy + n0) * Y::kSize;
+      if (16 * m < count) Y::template load<FULL>(at[m], g, a.N - n0, held[m]);
+    }
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void add(const LoraArgs& a, const ExpandSmem<DT, YT, RS>& sm, int n0, int count, float scale) {
+    const int l = threadIdx.x & 63, c = l & 15, g = l >> 4;
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) {
+      if (16 * m >= count) break;
+      const int t = min(16 * m + c, count - 1);
+      V piece[RS][kPieces];
+#pragma unroll
+      for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) piece[s][p] = sm.u[p][t][4 * s + g];
+      float v[16], by = scale;
+      if constexpr (DT == MXFP4_TYPE_F16) by = by * sm.back[t];
+      Y::unpack(held[m], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mx::v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < RS; ++s)
+#pragma unroll
+          for (int p = 0; p < kPieces; ++p) acc = Half<DT>::mfma(bv[j][s], piece[s][p], acc);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * j + e] = v[4 * j + e] + by * acc[e];
+      }
+      if (16 * m + c < count) Y::template store<FULL>(at[m], g, a.N - n0, v);
+    }
+  }
+};
+
+template <int DT, int YT, int RS>
+__global__ __launch_bounds__(kExpandThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F32) ? 2 : 3) void expand_kernel(LoraArgs a) {
+  typedef typename Half<DT>::V V;
   constexpr int kPieces = YT == MXFP4_TYPE_F32 ? 3 : 2;
   constexpr int kTiles = expand_tiles<YT, RS>();
-  // Ranks of a row in pieces of 8, one row 16 bytes longer than its ranks.
-  __shared__ V u[kPieces][16 * kTiles][4 * RS + 1];
-  __shared__ float back[16 * kTiles];  // undoes the power of two
-  const int tid = threadIdx.x, l = tid & 63, c = l & 15, g = l >> 4;
+  __shared__ __align__(16) ExpandSmem<DT, YT, RS> sm;
+  const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row0 = kBlock * blockIdx.y, n0 = kCols * blockIdx.x + 64 * wave;
   const int idx = adapter_of(a, row0);
@@ -403,7 +470,7 @@ __global__ __launch_bounds__(kExpandThreads, RS == 4 ? 2 : 3) void expand_kernel
           for (int d = kAdders; d < 4 * RS * kAdders; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
           const int up = top == 0 || top >= 0x7f800000u ? 0 : min(14 + 127 - (int)(top >> 23), 126);
           const float by = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
-          if (at == 0 && i % kAdders == 0 && t < count) back[t] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
+          if (at == 0 && i % kAdders == 0 && t < count) sm.back[t] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] *= by;
         }
@@ -416,62 +483,25 @@ __global__ __launch_bounds__(kExpandThreads, RS == 4 ? 2 : 3) void expand_kernel
               v[e] = Half<DT>::round(f[e]);
               f[e] = f[e] - (float)v[e];
             }
-            u[p][t][at] = v;
+            sm.u[p][t][at] = v;
           }
       }
     };
-    if (a.unit == 1)
+    if (a.splits > 12)
       sums(std::integral_constant<int, (RS == 4 ? 4 : 8)>());  // a row's threads are of one wave
     else
       sums(std::integral_constant<int, 1>());
-    // Row c of the operand of column group j is column Y::column(c / 4, j) + c % 4: result register e of
-    // group j of lane l is column Y::column(g, j) + e.
-    V bv[4][RS];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = min(n0 + Y::column(c >> 2, j) + (c & 3), a.N - 1);
-      const uint8_t* br = a.b + ((int64_t)adapter * a.N + n) * a.R * 2;
-#pragma unroll
-      for (int s = 0; s < RS; ++s) {
-        const int rank = 32 * s + 8 * g;
-        bv[j][s] = *reinterpret_cast<const V*>(br + (rank < a.R ? 2 * rank : 0));
-        if (rank >= a.R) bv[j][s] = V{0, 0, 0, 0, 0, 0, 0, 0};
-      }
-    }
-    uint8_t* at[kTiles];
-    uint32_t held[kTiles][Y::kWords];
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      if (16 * m >= count) break;
-      const int row = row0 + __shfl(order, first + min(16 * m + c, count - 1), 64);
-      at[m] = a.y + ((int64_t)row * a.ldy + n0) * Y::kSize;
-      if (16 * m + c < count) Y::load(at[m], g, a.N - n0, held[m]);
-    }
+    Columns<DT, YT, RS> columns;
+    const bool full = n0 + 64 <= a.N;  // the same for a wave
+    if (full)
+      columns.template load<true>(a, adapter, row0, n0, order, first, count);
+    else
+      columns.template load<false>(a, adapter, row0, n0, order, first, count);
     __syncthreads();
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      if (16 * m >= count) break;
-      const int t = min(16 * m + c, count - 1);
-      V piece[RS][kPieces];
-#pragma unroll
-      for (int s = 0; s < RS; ++s)
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) piece[s][p] = u[p][t][4 * s + g];
-      float v[16], by = scale;
-      if constexpr (DT == MXFP4_TYPE_F16) by = by * back[t];
-      Y::unpack(held[m], v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mx::v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < RS; ++s)
-#pragma unroll
-          for (int p = 0; p < kPieces; ++p) acc = Half<DT>::mfma(bv[j][s], piece[s][p], acc);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * j + e] = v[4 * j + e] + by * acc[e];
-      }
-      if (16 * m + c < count) Y::store(at[m], g, a.N - n0, v);
-    }
+    if (full)
+      columns.template add<true>(a, sm, n0, count, scale);
+    else
+      columns.template add<false>(a, sm, n0, count, scale);
   });
 }
 
@@ -487,10 +517,12 @@ int workgroups_of(int64_t T, int64_t n, int tiles, int64_t target) {
   const int64_t z = target / blocks;
   return (int)(z < 1 ? 1 : z > 8 ? (8 < most ? 8 : most) : (z < most ? z : most));
 }
-// Workgroups that share K: enough to occupy the chip, each wave one step of 32 at least.
+// Workgroups that share K: enough to occupy the chip, each wave one step of 32 at least; from 65
+// rows on at most 10, as every workgroup of expand adds up their sums (777 rows, K 2064, N 2113,
+// R 24: 17 splits 6.4 + 10.0 us for the two kernels, 9 splits 5.2 + 8.8).
 int splits_of(int64_t T, int64_t K) {
   const int64_t blocks = mxh::cdiv(T, kBlock), stages = mxh::cdiv(K, kStage), most = mxh::cdiv(stages, 2);
-  const int64_t want = blocks == 1 ? mxh::cdiv(512, T < 32 ? T : 32) : mxh::cdiv(256, blocks);
+  const int64_t want = blocks == 1 ? mxh::cdiv(512, T < 32 ? T : 32) : blocks < 26 ? 10 : mxh::cdiv(256, blocks);
   return (int)mxh::cdiv(stages, mxh::cdiv(stages, want < most ? want : most));
 }
 

@@ -8,6 +8,7 @@ these functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -579,8 +580,20 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 _I32, _U8, _BF16 = torch.int32, torch.uint8, torch.bfloat16
 
 
-def _scratch(nbytes: int, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(nbytes, dtype=_U8, device=like.device)
+# The library's size queries are pure functions of a few integers.
+@functools.lru_cache(maxsize=256)
+def _expert_bytes(I: int, H: int) -> tuple:
+    return int(lib().mxfp4_pack_B_bytes(2 * I, H)), int(lib().mxfp4_pack_B_bytes(H, I))
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_scratch(T: int, k: int, H: int, I: int) -> int:
+    return int(lib().moe_a16w4_workspace_bytes(T, k, H, I))
+
+
+@functools.lru_cache(maxsize=256)
+def _lora_scratch(T: int, K: int, R: int) -> int:
+    return int(lib().lora_add_workspace_bytes(T, K, R))
 
 
 def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
@@ -627,9 +640,8 @@ def pack_experts(bq: torch.Tensor, bs: torch.Tensor) -> torch.Tensor:
     return torch.stack([pack_B(q, s) for q, s in zip(bq, bs)])
 
 
-def _experts(p: torch.Tensor, name: str, N: int, K: int, dev: int):
+def _experts(p: torch.Tensor, name: str, need: int, N: int, K: int, dev: int):
     """(number of experts, bytes from one to the next) of packed expert weights."""
-    need = pack_B_bytes(N, K)
     if (p.dtype is not _U8 or p.get_device() != dev or p.dim() != 2 or need == 0 or p.shape[1] < need
             or p.stride(1) != 1):
         raise ValueError(f"{name} must be uint8 [E, {need}] (pack_experts of {N} x {K}) on device {dev}, "
@@ -649,22 +661,30 @@ def moe_a16w4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: to
     T, H = x.shape
     if ids.dim() != 2:
         raise ValueError("ids must be [T, k]")
-    k = ids.shape[1]
-    ldx = H if x.dtype is _BF16 and x.is_contiguous() else _matrix(x, "x", _BF16, T, H, dev)
-    _dense(ids, "ids", _I32, (T, k), dev)
-    _dense(weights, "weights", _F32, (T, k), dev)
-    E, stride13 = _experts(w13, "w13", 2 * I, H, dev)
-    E2, stride2 = _experts(w2, "w2", H, I, dev)
+    k, ldx = ids.shape[1], H
+    need13, need2 = _expert_bytes(I, H)
+    if (x.dtype is _BF16 and ids.dtype is _I32 and weights.dtype is _F32 and w13.dtype is _U8 and w2.dtype is _U8
+            and x.is_contiguous() and ids.is_contiguous() and weights.is_contiguous() and w13.is_contiguous()
+            and w2.is_contiguous() and ids.get_device() == dev and weights.get_device() == dev
+            and w13.get_device() == dev and w2.get_device() == dev and ids.shape[0] == T and weights.shape == ids.shape
+            and need13 and w13.dim() == 2 and w2.dim() == 2 and w13.shape[1] >= need13 and w2.shape[1] >= need2):
+        (E, stride13), (E2, stride2) = w13.shape, w2.shape
+    else:
+        ldx = _matrix(x, "x", _BF16, T, H, dev)
+        _dense(ids, "ids", _I32, (T, k), dev)
+        _dense(weights, "weights", _F32, (T, k), dev)
+        E, stride13 = _experts(w13, "w13", need13, 2 * I, H, dev)
+        E2, stride2 = _experts(w2, "w2", need2, H, I, dev)
     if E != E2:
         raise ValueError(f"w13 has {E} experts and w2 {E2}")
+    device = x.device
     if out is None:
-        out, ldy = torch.empty(T, H, dtype=_BF16, device=x.device), H
+        out, ldy = torch.empty(T, H, dtype=_BF16, device=device), H
     else:
         ldy = _matrix(out, "out", _BF16, T, H, dev)
-    L = _lib or lib()
-    nbytes = L.moe_a16w4_workspace_bytes(T, k, H, I)
-    ws = _scratch(nbytes, x)
-    _call(L.moe_a16w4, "moe_a16w4", dev,
+    nbytes = _moe_scratch(T, k, H, I)
+    ws = torch.empty(nbytes, dtype=_U8, device=device)
+    _call((_lib or lib()).moe_a16w4, "moe_a16w4", dev,
           (x.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), w13.data_ptr(), stride13, w2.data_ptr(), stride2,
            out.data_ptr(), ldy, T, k, E, H, I, ws.data_ptr(), nbytes, _raw_stream(dev)))
     return out
@@ -680,23 +700,23 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if x.dim() != 2 or a.dim() != 3:
         raise ValueError("x must be [T, K] and a [n, R, K]")
     D, K = x.dtype, x.shape[1]
-    n, R = a.shape[0], a.shape[1]
-    ldy = N if y.is_contiguous() else _matrix(y, "y", y.dtype, T, N, dev)
-    if not (x.get_device() == dev and x.shape[0] == T and x.is_contiguous()):
+    n, R, ldx, ldy = a.shape[0], a.shape[1], K, N
+    if not (y.is_contiguous() and x.is_contiguous() and a.is_contiguous() and b.is_contiguous()
+            and index.is_contiguous() and a.dtype is D and b.dtype is D and index.dtype is _I32
+            and x.get_device() == dev and a.get_device() == dev and b.get_device() == dev and index.get_device() == dev
+            and x.shape[0] == T and a.shape[2] == K and b.shape == (n, N, R) and index.shape == (T,)):
+        ldy = _matrix(y, "y", y.dtype, T, N, dev)
         ldx = _matrix(x, "x", D, T, K, dev)
-    else:
-        ldx = K
-    _dense(a, "a", D, (n, R, K), dev)
-    _dense(b, "b", D, (n, N, R), dev)
-    _vector(index, "index", _I32, T, dev)
+        _dense(a, "a", D, (n, R, K), dev)
+        _dense(b, "b", D, (n, N, R), dev)
+        _vector(index, "index", _I32, T, dev)
     sp = None
     if scale is not None:
         _vector(scale, "scale", _F32, n, dev)
         sp = scale.data_ptr()
-    L = _lib or lib()
-    nbytes = L.lora_add_workspace_bytes(T, K, R)
-    ws = _scratch(nbytes, x)
-    _call(L.lora_add, "lora_add", dev,
+    nbytes = _lora_scratch(T, K, R)
+    ws = torch.empty(nbytes, dtype=_U8, device=y.device)
+    _call((_lib or lib()).lora_add, "lora_add", dev,
           (y.data_ptr(), ldy, yt, x.data_ptr(), ldx, TYPES.get(D, -1), a.data_ptr(), b.data_ptr(), index.data_ptr(), sp,
            T, N, K, R, n, ws.data_ptr(), nbytes, _raw_stream(dev)))
     return y

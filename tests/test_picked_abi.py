@@ -105,10 +105,10 @@ def test_binding_refuses_what_it_cannot_marshal():
     with pytest.raises(ValueError, match="contiguous torch.int32"):
         ops._dense(i.t(), "ids", torch.int32, (2, 2), 0)
     with pytest.raises(ValueError, match="pack_experts of 64 x 32"):
-        ops._experts(w[:, :100], "w13", 64, 32, -1)
+        ops._experts(w[:, :100], "w13", 2304, 64, 32, -1)
     with pytest.raises(ValueError, match="pack_experts of 64 x 33"):
-        ops._experts(w, "w13", 64, 33, -1)
-    assert ops._experts(w[:, :2600], "w13", 64, 32, -1) == (3, 4096)
+        ops._experts(w, "w13", 0, 64, 33, -1)
+    assert ops._experts(w[:, :2600], "w13", 2304, 64, 32, -1) == (3, 4096)
 
 
 def test_plain_forms_dequantise_as_the_oracle():
