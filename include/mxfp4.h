@@ -552,13 +552,13 @@ int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const float* weigh
  *   a : [n, R, K] and b : [n, N, R] of type xtype, contiguous.
  *       x, ldx * 2 bytes, a and b multiples of 16 bytes; ldx <= 2^36.
  *   index : int32 [T];  scale : fp32 [n], or NULL for 1.
- *   T, n >= 1, T <= 2^20, n <= 2^20; K % 8 == 0, 8 <= K <= 2^20; R % 8 == 0,
+ *   T, n >= 1, T <= 2^20, n <= 4096; K % 8 == 0, 8 <= K <= 2^20; R % 8 == 0,
  *   8 <= R <= 128; 1 <= N <= 2^20. y overlaps no other argument. Adapters of
  *   smaller rank are padded with rows (A) and columns (B) of zeros.
- *   workspace : >= lora_add_workspace_bytes(T, K, R), 16-byte aligned, any
+ *   workspace : >= lora_add_workspace_bytes(T, K, R, n), 16-byte aligned, any
  *       contents; scratch during the call only. (0 for a rejected shape.)
  * ------------------------------------------------------------------------- */
-size_t lora_add_workspace_bytes(int64_t T, int64_t K, int64_t R);
+size_t lora_add_workspace_bytes(int64_t T, int64_t K, int64_t R, int64_t n);
 int lora_add(void* y, int64_t ldy, int ytype, const void* x, int64_t ldx, int xtype, const void* a, const void* b,
              const int32_t* index, const float* scale, int64_t T, int64_t N, int64_t K, int64_t R, int64_t n,
              void* workspace, size_t workspace_bytes, void* stream);

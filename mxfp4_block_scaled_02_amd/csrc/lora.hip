@@ -1,11 +1,11 @@
 // lora_add: y[t] += scale * (x[t] . A^T) . B^T with the adapter (A, B) of each row, for
 // low-rank adapters of many requests beside a shared projection.
 //
-// Two launches. shrink: x . A^T in fp32 partial sums [split][T][R]. expand: 512 columns to
-// a workgroup, which adds the partial sums in their order, holds them as 16-bit pieces and
-// multiplies with B. Both take 64 neighbouring rows and an adapter at a time: the rows that
-// have it are gathered into 16-row tiles, so that A and B are read once for all of them, and
-// no row meets another one's adapter.
+// shrink: x . A^T in fp32 partial sums [split][T][R]. expand: 256 columns to a workgroup, which
+// adds the partial sums in their order, holds them as 16-bit pieces and multiplies with B. Both
+// take units of up to 64 rows with the same adapter, wherever they lie among the rows, in 16-row
+// tiles: A and B are read once for a unit, and no row meets another one's adapter. The units of
+// up to 64 rows are found by every wave itself; of more by a launch in front (plan).
 #include "host_common.hpp"
 #include "mx_device.hpp"
 
@@ -17,12 +17,16 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 
-constexpr int kBlock = 64;          // rows, one to a lane
+constexpr int kFew = 64;            // rows of a call that a wave looks through by itself
+constexpr int kBlock = 4096;        // rows of a block of plan
+constexpr int kMaxN = 4096;
+constexpr int kUnit = 64;           // rows with one adapter that go together at most
+constexpr int kThreads = 256;
 constexpr int kStage = 64;          // k of a step of shrink: 128 bytes, a cache line of a row
 constexpr int kShrinkWaves = 4;
-constexpr int kShrinkThreads = 64 * kShrinkWaves;
+static_assert(kThreads == 64 * kShrinkWaves);
 constexpr int kExpandWaves = 4;
-constexpr int kExpandThreads = 64 * kExpandWaves;
+static_assert(kThreads == 64 * kExpandWaves);
 constexpr int kCols = 64 * kExpandWaves;  // columns of y to a workgroup of expand
 
 struct LoraArgs {
@@ -37,6 +41,8 @@ struct LoraArgs {
   float* part;
   int T, N, K, R, n;
   int unit;           // 16-row tiles that a workgroup of expand takes together
+  struct Unit* units;
+  int slots;          // units that a block may have
   int splits, slice;  // workgroups that share K, steps of kStage to each
 };
 
@@ -60,47 +66,130 @@ struct Half<MXFP4_TYPE_F16> {
   static __device__ __forceinline__ _Float16 round(float f) { return (_Float16)f; }
 };
 
-// The adapter of lane l's row, -1 without one.
-__device__ __forceinline__ int adapter_of(const LoraArgs& a, int row0) {
-  const int row = row0 + (threadIdx.x & 63);
+// The adapter of a row, -1 without one.
+__device__ __forceinline__ int adapter_of(const LoraArgs& a, int row) {
   const int i = row < a.T ? a.index[row] : -1;
   return (uint32_t)i < (uint32_t)a.n ? i : -1;
 }
-// The groups of rows (of the 64) with the same adapter, in units of `tiles` 16-row tiles, of
-// which gridDim.z workgroups take every gridDim.z-th; f(adapter, rows, first) is called by all
-// waves alike, first the unit's first row within its group. One block of rows has a workgroup
-// for each row instead, which goes on if its row is the first of a unit: the count of units
-// before it need not be known.
-template <typename F>
-__device__ __forceinline__ void for_units(const LoraArgs& a, int idx, int tiles, F f) {
-  if (gridDim.y == 1) {
+// Up to 64 rows with one adapter.
+struct __align__(16) Unit {
+  int adapter, count;     // no rows in a slot that is not needed
+  uint16_t rows[kUnit];   // within the block
+};
+// At most: a unit for every 64 rows, and one that is not full for each adapter.
+__host__ __device__ inline int64_t slots_of(int64_t T, int64_t n) {
+  const int64_t here = T < kBlock ? T : kBlock;
+  return here / kUnit + (n < here ? n : here);
+}
+
+// The units of a block of rows, by rising adapter, the rows of each in an order that the indices
+// alone decide: a counting sort. A wave counts the adapters of its rows (every 16th run of 64),
+// the counts are added up over the waves, and over the adapters the units. TIMES
+constexpr int kPlanWaves = 16;
+template <int kWords>  // runs of 64 rows to a wave
+__global__ __launch_bounds__(64 * kPlanWaves) void plan_kernel(LoraArgs a) {
+  __shared__ uint16_t before[kPlanWaves][kMaxN];  // rows with the adapter in the waves before
+  __shared__ uint16_t unit0[kMaxN];               // the adapter's first unit
+  __shared__ int sums[kPlanWaves];
+  const int tid = threadIdx.x, l = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint64_t below = ((uint64_t)1 << l) - 1;
+  const int row0 = kBlock * blockIdx.x;
+  auto row_of = [&](int w) { return 64 * (kPlanWaves * w + wave) + l; };
+  Unit* const units = a.units + (int64_t)blockIdx.x * a.slots;
+  int idx[kWords], rank[kWords];
+  uint64_t todo[kWords];
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) idx[w] = adapter_of(a, row0 + row_of(w));
+  for (int i = l; i < a.n; i += 64) before[wave][i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) todo[w] = __ballot(idx[w] >= 0);
+  for (;;) {
+    uint64_t any = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) any |= todo[w];
+    if (any == 0) break;
+    int adapter = 0, total = 0;
+#pragma unroll
+    for (int w = kWords - 1; w >= 0; --w)
+      if (todo[w]) adapter = __builtin_amdgcn_readlane(idx[w], __ffsll((unsigned long long)todo[w]) - 1);
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const bool match = idx[w] == adapter;
+      const uint64_t rows = __ballot(match);
+      todo[w] &= ~rows;
+      if (match) rank[w] = total + __popcll(rows & below);
+      total += __popcll(rows);
+    }
+    if (l == 0) before[wave][adapter] = (uint16_t)total;
+  }
+  __syncthreads();
+  int units_before = 0;  // of the adapters of the rounds before
+  for (int i0 = 0; i0 < a.n; i0 += 64 * kPlanWaves) {
+    const int i = i0 + tid;
+    int total = 0;
+    if (i < a.n)
+#pragma unroll
+      for (int w = 0; w < kPlanWaves; ++w) {
+        const int c = before[w][i];
+        before[w][i] = (uint16_t)total;
+        total += c;
+      }
+    const int count = (total + kUnit - 1) / kUnit;
+    int upto = count;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(upto, d, 64);
+      if (l >= d) upto += o;
+    }
+    if (l == 63) sums[wave] = upto;
+    __syncthreads();
+    int first = units_before + upto - count;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      if (w < wave) first += sums[w];
+      units_before += sums[w];
+    }
+    if (i < a.n) unit0[i] = (uint16_t)first;
+    for (int u = 0; u < count; ++u) {
+      units[first + u].adapter = i;
+      units[first + u].count = min(total - kUnit * u, kUnit);
+    }
+    __syncthreads();
+  }
+  for (int u = units_before + tid; u < a.slots; u += 64 * kPlanWaves) units[u].count = 0;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w)
+    if (idx[w] >= 0) {
+      const int at = before[wave][idx[w]] + rank[w];
+      units[unit0[idx[w]] + at / kUnit].rows[at % kUnit] = (uint16_t)row_of(w);
+    }
+}
+
+// Calls f(adapter, row0, order, count) for the unit of this workgroup, if it has one, by all waves
+// alike: lane p < count's `order` is the unit's p-th row, from row0 on. Units are taken apart into
+// pieces of up to `size` rows. FEW (T <= 64): a workgroup (blockIdx.z) for each row, which goes on
+// if its row is the first of a piece.
+template <bool FEW, typename F>
+__device__ __forceinline__ void with_unit(const LoraArgs& a, int size, F f) {
+  const int l = threadIdx.x & 63;
+  if constexpr (FEW) {
+    const int idx = adapter_of(a, l);
     const int r = blockIdx.z, adapter = __builtin_amdgcn_readlane(idx, r);
     if (adapter < 0) return;
-    const uint64_t rows = __ballot(idx == adapter);
-    const int before = __popcll(rows & (((uint64_t)1 << r) - 1));
-    if (before % (16 * tiles) == 0) f(adapter, rows, before);
-    return;
+    const uint64_t rows = __ballot(idx == adapter), below = ((uint64_t)1 << l) - 1;
+    const int first = __popcll(rows & (((uint64_t)1 << r) - 1));
+    if (first % size != 0) return;
+    // Lane p gets the p-th of the rows (past the last one: some other row), then the first + p-th.
+    const int at = (rows >> l) & 1 ? __popcll(rows & below) : __popcll(rows) + __popcll(~rows & below);
+    const int order = __builtin_amdgcn_ds_permute(4 * at, l);
+    f(adapter, 0, __shfl(order, min(first + l, 63), 64), min(__popcll(rows) - first, size));
+  } else {
+    const int pieces = kUnit / size, first = (int)(blockIdx.z % pieces) * size;
+    const Unit& u = a.units[(int64_t)blockIdx.y * a.slots + blockIdx.z / pieces];
+    const int adapter = u.adapter, count = min(u.count - first, size), order = u.rows[min(first + l, kUnit - 1)];
+    if (count > 0) f(adapter, kBlock * (int)blockIdx.y, order, count);
   }
-  int turn = blockIdx.z;
-  for (uint64_t todo = __ballot(idx >= 0); todo != 0;) {
-    const int adapter = __builtin_amdgcn_readlane(idx, __ffsll((unsigned long long)todo) - 1);
-    const uint64_t rows = __ballot(idx == adapter);
-    todo &= ~rows;
-    for (int first = 0; first < __popcll(rows); first += 16 * tiles) {
-      if (turn == 0) {
-        f(adapter, rows, first);
-        turn = gridDim.z;
-      }
-      --turn;
-    }
-  }
-}
-// Lane p gets the p-th of the rows (past the last one: some other row).
-__device__ __forceinline__ int gathered(uint64_t rows) {
-  const int l = threadIdx.x & 63;
-  const uint64_t below = ((uint64_t)1 << l) - 1;
-  const int at = (rows >> l) & 1 ? __popcll(rows & below) : __popcll(rows) + __popcll(~rows & below);
-  return __builtin_amdgcn_ds_permute(4 * at, l);
 }
 
 // More than 16 rows (R <= 16 RT): rows of x and of A go through LDS a step at a time, as whole
@@ -112,23 +201,23 @@ __device__ __forceinline__ int gathered(uint64_t rows) {
 constexpr int kAhead = 4;
 template <int RT>
 struct TileSmem {
-  u32x4 line[2][kBlock + 16 * RT][8];
+  u32x4 line[2][kUnit + 16 * RT][8];
 };
 template <int DT, int RT>
 __device__ __forceinline__ void shrink_tile(const LoraArgs& a, int adapter, int row0, int order, int count, int begin,
                                             int end, TileSmem<RT>& sm, mx::v4f (&acc)[RT]) {
   typedef typename Half<DT>::V V;
-  constexpr int kLoads = (8 * (kBlock + 16 * RT) + kShrinkThreads - 1) / kShrinkThreads;
-  constexpr int kRows = kShrinkThreads / 8;  // rows that a load of all threads covers
+  constexpr int kLoads = (8 * (kUnit + 16 * RT) + kThreads - 1) / kThreads;
+  constexpr int kRows = kThreads / 8;  // rows that a load of all threads covers
   const int tid = threadIdx.x, l = tid & 63, c = l & 15, g = l >> 4, wave = tid >> 6;
   const int p = tid & 7, slot = p ^ ((tid >> 4) & 7);
   const uint8_t* src[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int r = kRows * i + (tid >> 3);
-    src[i] = i < kBlock / kRows
+    src[i] = i < kUnit / kRows
                  ? a.x + (int64_t)(row0 + __shfl(order, min(r, count - 1), 64)) * a.ldx
-                 : a.a + ((int64_t)adapter * a.R + min(r - kBlock, a.R - 1)) * a.K * 2;
+                 : a.a + ((int64_t)adapter * a.R + min(r - kUnit, a.R - 1)) * a.K * 2;
   }
   // Steps past the end are zeros: the loop has no branch around a load, so that the waits count
   // the loads that are under way.
@@ -144,7 +233,7 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, int adapter, int 
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int r = kRows * i + (tid >> 3);
-      if (r < kBlock + 16 * RT) sm.line[buf][r][slot] = in || i >= kBlock / kRows ? v[i] : u32x4{0, 0, 0, 0};
+      if (r < kUnit + 16 * RT) sm.line[buf][r][slot] = in || i >= kUnit / kRows ? v[i] : u32x4{0, 0, 0, 0};
     }
   };
 #pragma unroll
@@ -163,7 +252,7 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, int adapter, int 
         const int at = (4 * kk + g) ^ ((c >> 1) & 7);
         xv[kk] = __builtin_bit_cast(V, sm.line[i & 1][16 * wave + c][at]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) av[kk][r] = __builtin_bit_cast(V, sm.line[i & 1][kBlock + 16 * r + c][at]);
+        for (int r = 0; r < RT; ++r) av[kk][r] = __builtin_bit_cast(V, sm.line[i & 1][kUnit + 16 * r + c][at]);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -206,19 +295,17 @@ __device__ __forceinline__ void shrink_few(const LoraArgs& a, int adapter, int r
   }
 }
 
-template <int DT, int RT, int U>
-__global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(LoraArgs a) {
+template <int DT, int RT, int U, bool FEW>
+__global__ __launch_bounds__(kThreads) void shrink_kernel(LoraArgs a) {
   __shared__ union {
     TileSmem<RT> tile;
     mx::v4f red[kShrinkWaves][RT][64];
   } sm;
   const int tid = threadIdx.x, l = tid & 63, c = l & 15, g = l >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int row0 = kBlock * blockIdx.y, q = blockIdx.x;
-  const int idx = adapter_of(a, row0);
+  const int q = blockIdx.x;
   const int stages = (a.K + kStage - 1) / kStage, begin = q * a.slice, end = min(begin + a.slice, stages);
-  for_units(a, idx, kBlock / 16, [&](int adapter, uint64_t rows, int) {
-    const int order = gathered(rows), count = __popcll(rows);
+  with_unit<FEW>(a, kUnit, [&](int adapter, int row0, int order, int count) {
     mx::v4f acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r] = mx::v4f{0.f, 0.f, 0.f, 0.f};
@@ -371,7 +458,7 @@ struct Columns {
   uint32_t held[kTiles][Y::kWords];
 
   template <bool FULL>
-  __device__ __forceinline__ void load(const LoraArgs& a, int adapter, int row0, int n0, int order, int first, int count) {
+  __device__ __forceinline__ void load(const LoraArgs& a, int adapter, int row0, int n0, int order, int count) {
     const int l = threadIdx.x & 63, c = l & 15, g = l >> 4;
     // Row c of the operand of column group j is column Y::column(c / 4, j) + c % 4: result register e of
     // group j of lane l is column Y::column(g, j) + e. Past R the pieces are zeros, and B's are any.
@@ -387,7 +474,7 @@ struct Columns {
     }
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) {
-      const int row = row0 + __shfl(order, first + min(16 * m + c, count - 1), 64);
+      const int row = row0 + __shfl(order, min(16 * m + c, count - 1), 64);
       at[m] = a.y + ((int64_t)row * a.ldy + n0) * Y::kSize;
       if (16 * m < count) Y::template load<FULL>(at[m], g, a.N - n0, held[m]);
     }
@@ -422,28 +509,26 @@ struct Columns {
   }
 };
 
-template <int DT, int YT, int RS>
-__global__ __launch_bounds__(kExpandThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F32) ? 2 : 3) void expand_kernel(LoraArgs a) {
+template <int DT, int YT, int RS, bool FEW>
+__global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F32) ? 2 : 3) void expand_kernel(LoraArgs a) {
   typedef typename Half<DT>::V V;
   constexpr int kPieces = YT == MXFP4_TYPE_F32 ? 3 : 2;
   constexpr int kTiles = expand_tiles<YT, RS>();
   __shared__ __align__(16) ExpandSmem<DT, YT, RS> sm;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int row0 = kBlock * blockIdx.y, n0 = kCols * blockIdx.x + 64 * wave;
-  const int idx = adapter_of(a, row0);
-  for_units(a, idx, a.unit, [&](int adapter, uint64_t rows, int first) {
-    const int order = gathered(rows), count = min(__popcll(rows) - first, 16 * a.unit);
+  const int n0 = kCols * blockIdx.x + 64 * wave;
+  with_unit<FEW>(a, 16 * a.unit, [&](int adapter, int row0, int order, int count) {
     const float scale = a.scale ? a.scale[adapter] : 1.0f;
     __syncthreads();
     // 8 ranks of a row to kAdders neighbouring threads, which share the partial sums; 4 RS such
     // groups to a row.
     auto sums = [&](auto adders) {
       constexpr int kAdders = decltype(adders)::value;
-      for (int i0 = 0; i0 < 64 * kTiles * RS * kAdders; i0 += kExpandThreads) {
+      for (int i0 = 0; i0 < 64 * kTiles * RS * kAdders; i0 += kThreads) {
         const int i = i0 + tid, t = i / (4 * RS * kAdders), at = i / kAdders % (4 * RS);
         if (i0 >= 4 * RS * kAdders * count) break;
-        const int row = row0 + __shfl(order, min(first + t, kBlock - 1), 64);
+        const int row = row0 + __shfl(order, min(t, count - 1), 64);
         float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (t < count && 8 * at < a.R) {
           const float* p = a.part + (int64_t)row * a.R + 8 * at;
@@ -494,9 +579,9 @@ __global__ __launch_bounds__(kExpandThreads, RS == 4 || (RS == 2 && YT == MXFP4_
     Columns<DT, YT, RS> columns;
     const bool full = n0 + 64 <= a.N;  // the same for a wave
     if (full)
-      columns.template load<true>(a, adapter, row0, n0, order, first, count);
+      columns.template load<true>(a, adapter, row0, n0, order, count);
     else
-      columns.template load<false>(a, adapter, row0, n0, order, first, count);
+      columns.template load<false>(a, adapter, row0, n0, order, count);
     __syncthreads();
     if (full)
       columns.template add<true>(a, sm, n0, count, scale);
@@ -505,46 +590,52 @@ __global__ __launch_bounds__(kExpandThreads, RS == 4 || (RS == 2 && YT == MXFP4_
   });
 }
 
-bool shape_ok(int64_t T, int64_t K, int64_t R) {
+bool shape_ok(int64_t T, int64_t K, int64_t R, int64_t n) {
   constexpr int64_t kMax = (int64_t)1 << 20;
-  return T >= 1 && T <= kMax && K >= 8 && K <= kMax && K % 8 == 0 && R >= 8 && R <= 128 && R % 8 == 0;
-}
-// Workgroups that share a block's units of `tiles` row tiles (see for_units). Most blocks of a
-// prompt have one group, some two; a decode batch has as many as it has rows or adapters.
-int workgroups_of(int64_t T, int64_t n, int tiles, int64_t target) {
-  const int64_t blocks = mxh::cdiv(T, kBlock), most = kBlock / 16 / tiles + n - 1;
-  if (blocks == 1) return (int)T;
-  const int64_t z = target / blocks;
-  return (int)(z < 1 ? 1 : z > 8 ? (8 < most ? 8 : most) : (z < most ? z : most));
+  return T >= 1 && T <= kMax && K >= 8 && K <= kMax && K % 8 == 0 && R >= 8 && R <= 128 && R % 8 == 0 &&
+         n >= 1 && n <= kMaxN;
 }
 // Workgroups that share K: enough to occupy the chip, each wave one step of 32 at least; from 65
 // rows on at most 10, as every workgroup of expand adds up their sums (777 rows, K 2064, N 2113,
 // R 24: 17 splits 6.4 + 10.0 us for the two kernels, 9 splits 5.2 + 8.8).
 int splits_of(int64_t T, int64_t K) {
-  const int64_t blocks = mxh::cdiv(T, kBlock), stages = mxh::cdiv(K, kStage), most = mxh::cdiv(stages, 2);
-  const int64_t want = blocks == 1 ? mxh::cdiv(512, T < 32 ? T : 32) : blocks < 26 ? 10 : mxh::cdiv(256, blocks);
+  const int64_t stages = mxh::cdiv(K, kStage), most = mxh::cdiv(stages, 2);
+  const int64_t want = T <= kFew ? mxh::cdiv(512, T < 32 ? T : 32) : T < 26 * 64 ? 10 : mxh::cdiv(16384, T);
   return (int)mxh::cdiv(stages, mxh::cdiv(stages, want < most ? want : most));
 }
 
+// The grid's y and z for pieces of `rows` rows (see with_unit).
+dim3 grid_of(const LoraArgs& a, unsigned x, int rows) {
+  if (a.T <= kFew) return dim3(x, 1, (unsigned)a.T);
+  return dim3(x, (unsigned)mxh::cdiv(a.T, kBlock), (unsigned)(a.slots * (kUnit / rows)));
+}
 template <int DT, int RT, int U>
 hipError_t launch_shrink(LoraArgs& a, hipStream_t st) {
   void* args[] = {&a};
-  return hipLaunchKernel((const void*)shrink_kernel<DT, RT, U>,
-                         dim3((unsigned)a.splits, (unsigned)mxh::cdiv(a.T, kBlock), (unsigned)workgroups_of(a.T, a.n, kBlock / 16, 256)),
-                         dim3(kShrinkThreads), args, 0, st);
+  return hipLaunchKernel(a.T <= kFew ? (const void*)shrink_kernel<DT, RT, U, true> : (const void*)shrink_kernel<DT, RT, U, false>,
+                         grid_of(a, (unsigned)a.splits, kUnit), dim3(kThreads), args, 0, st);
 }
 template <int DT, int YT, int RS>
 hipError_t launch_expand(LoraArgs& a, hipStream_t st) {
   a.unit = a.T <= 2048 ? 1 : expand_tiles<YT, RS>();
   void* args[] = {&a};
-  return hipLaunchKernel((const void*)expand_kernel<DT, YT, RS>,
-                         dim3((unsigned)mxh::cdiv(a.N, kCols), (unsigned)mxh::cdiv(a.T, kBlock),
-                              (unsigned)workgroups_of(a.T, a.n, a.unit, a.unit == 1 ? 256 : 128)),
-                         dim3(kExpandThreads), args, 0, st);
+  return hipLaunchKernel(a.T <= kFew ? (const void*)expand_kernel<DT, YT, RS, true> : (const void*)expand_kernel<DT, YT, RS, false>,
+                         grid_of(a, (unsigned)mxh::cdiv(a.N, kCols), 16 * a.unit), dim3(kThreads), args, 0, st);
 }
+size_t part_bytes(int64_t T, int64_t K, int64_t R) { return (size_t)splits_of(T, K) * (size_t)T * (size_t)R * 4; }
+
 template <int DT, int YT>
 int launch(LoraArgs& a, hipStream_t st) {
-  hipError_t e = a.R <= 16   ? launch_shrink<DT, 1, 4>(a, st)
+  hipError_t e = hipSuccess;
+  if (a.T > kFew) {
+    void* args[] = {&a};
+    const void* f = a.T <= 1024   ? (const void*)plan_kernel<1>
+                    : a.T <= 2048 ? (const void*)plan_kernel<2>
+                                  : (const void*)plan_kernel<kBlock / (64 * kPlanWaves)>;
+    e = hipLaunchKernel(f, dim3((unsigned)mxh::cdiv(a.T, kBlock)), dim3(64 * kPlanWaves), args, 0, st);
+    if (e != hipSuccess) return MXFP4_ERR_HIP;
+  }
+  e = a.R <= 16   ? launch_shrink<DT, 1, 4>(a, st)
                  : a.R <= 32 ? launch_shrink<DT, 2, 4>(a, st)
                  : a.R <= 64 ? launch_shrink<DT, 4, 4>(a, st)
                              : launch_shrink<DT, 8, 2>(a, st);
@@ -557,8 +648,9 @@ int launch(LoraArgs& a, hipStream_t st) {
 
 }  // namespace
 
-extern "C" size_t lora_add_workspace_bytes(int64_t T, int64_t K, int64_t R) {
-  return shape_ok(T, K, R) ? (size_t)splits_of(T, K) * (size_t)T * (size_t)R * 4 : 0;
+extern "C" size_t lora_add_workspace_bytes(int64_t T, int64_t K, int64_t R, int64_t n) {
+  if (!shape_ok(T, K, R, n)) return 0;
+  return part_bytes(T, K, R) + (T <= kFew ? 0 : (size_t)(mxh::cdiv(T, kBlock) * slots_of(T, n)) * sizeof(Unit));
 }
 
 extern "C" int lora_add(void* y, int64_t ldy, int ytype, const void* x, int64_t ldx, int xtype, const void* a,
@@ -569,17 +661,17 @@ extern "C" int lora_add(void* y, int64_t ldy, int ytype, const void* x, int64_t 
   if (xtype != MXFP4_TYPE_BF16 && xtype != MXFP4_TYPE_F16) return MXFP4_ERR_ARG;
   if (ytype != xtype && ytype != MXFP4_TYPE_F32) return MXFP4_ERR_ARG;
   constexpr int64_t kMax = (int64_t)1 << 20, kMaxLd = (int64_t)1 << 36;
-  if (!shape_ok(T, K, R) || N > kMax || n > kMax || ldx < K || ldx > kMaxLd || ldy < N || ldy > kMaxLd)
+  if (!shape_ok(T, K, R, n) || N > kMax || ldx < K || ldx > kMaxLd || ldy < N || ldy > kMaxLd)
     return MXFP4_ERR_SHAPE;
   if (!mxh::aligned(x, 16) || ldx % 8 != 0 || !mxh::aligned(a, 16) || !mxh::aligned(b, 16) ||
       !mxh::aligned(y, ytype == MXFP4_TYPE_F32 ? 4 : 2) || !mxh::aligned(index, 4) || !mxh::aligned(scale, 4))
     return MXFP4_ERR_ALIGN;
-  if (!workspace || !mxh::aligned(workspace, 16) || workspace_bytes < lora_add_workspace_bytes(T, K, R))
+  if (!workspace || !mxh::aligned(workspace, 16) || workspace_bytes < lora_add_workspace_bytes(T, K, R, n))
     return MXFP4_ERR_WORKSPACE;
   const int splits = splits_of(T, K);
   LoraArgs p{(uint8_t*)y, ldy,   (const uint8_t*)x, ldx * 2, (const uint8_t*)a, (const uint8_t*)b, index, scale,
              (float*)workspace, (int)T, (int)N, (int)K, (int)R, (int)n,
-             0, splits, (int)mxh::cdiv(mxh::cdiv(K, kStage), splits)};
+             0, (Unit*)((uint8_t*)workspace + part_bytes(T, K, R)), (int)slots_of(T, n), splits, (int)mxh::cdiv(mxh::cdiv(K, kStage), splits)};
   const hipStream_t st = (hipStream_t)stream;
   if (xtype == MXFP4_TYPE_BF16)
     return ytype == MXFP4_TYPE_F32 ? launch<MXFP4_TYPE_BF16, MXFP4_TYPE_F32>(p, st)

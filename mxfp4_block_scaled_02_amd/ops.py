@@ -116,7 +116,7 @@ def lib() -> ctypes.CDLL:
         L.moe_a16w4_workspace_bytes.argtypes, L.moe_a16w4_workspace_bytes.restype = [i64] * 4, sz
         L.moe_a16w4.argtypes = [vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, sz, vp]
         L.moe_a16w4.restype = i32
-        L.lora_add_workspace_bytes.argtypes, L.lora_add_workspace_bytes.restype = [i64] * 3, sz
+        L.lora_add_workspace_bytes.argtypes, L.lora_add_workspace_bytes.restype = [i64] * 4, sz
         L.lora_add.argtypes = [vp, i64, i32, vp, i64, i32, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, sz, vp]
         L.lora_add.restype = i32
         _lib = L
@@ -592,8 +592,8 @@ def _moe_scratch(T: int, k: int, H: int, I: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _lora_scratch(T: int, K: int, R: int) -> int:
-    return int(lib().lora_add_workspace_bytes(T, K, R))
+def _lora_scratch(T: int, K: int, R: int, n: int) -> int:
+    return int(lib().lora_add_workspace_bytes(T, K, R, n))
 
 
 def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
@@ -714,7 +714,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     if scale is not None:
         _vector(scale, "scale", _F32, n, dev)
         sp = scale.data_ptr()
-    nbytes = _lora_scratch(T, K, R)
+    nbytes = _lora_scratch(T, K, R, n)
     ws = torch.empty(nbytes, dtype=_U8, device=y.device)
     _call((_lib or lib()).lora_add, "lora_add", dev,
           (y.data_ptr(), ldy, yt, x.data_ptr(), ldx, TYPES.get(D, -1), a.data_ptr(), b.data_ptr(), index.data_ptr(), sp,

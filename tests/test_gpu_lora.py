@@ -46,7 +46,8 @@ TYPES = [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (tor
 @pytest.mark.parametrize("T,K,N,R,n", [
     (1, 8, 1, 8, 1), (1, 512, 256, 16, 4), (1, 7168, 2112, 16, 8), (3, 40, 17, 8, 2), (16, 128, 64, 24, 3),
     (17, 136, 65, 32, 40), (64, 2048, 300, 40, 24), (100, 264, 1023, 64, 7), (33, 1000, 257, 72, 5), (50, 96, 511, 128, 3),
-    (777, 520, 333, 24, 5), (2049, 64, 48, 104, 9),
+    (777, 520, 333, 24, 5), (2049, 64, 48, 104, 9), (65, 72, 40, 8, 3),
+    (256, 96, 70, 16, 60), (300, 64, 33, 8, 300), (2100, 136, 130, 16, 2),
 ])
 def test_adapters(T, K, N, R, n, dtype, out):
     check(case(T + K + N, T, K, N, R, n, dtype, out))
@@ -147,3 +148,58 @@ def test_beside_a_quantised_projection_captured_and_replayed():
         assert torch.equal(y, eager)
         ref, bound = picked.adapters(ops.gemm(c["x"], bp, N), c["x"], c["a"], c["b"], c["index"], c["scale"])
         assert ((y.double() - ref).abs() <= bound).all()
+
+
+def test_workspace_contents_do_not_matter_and_its_end_is_kept():
+    """The C call with a workspace of NaNs, and bytes behind it that stay."""
+    for T, n in ((3, 2), (64, 5), (65, 5), (300, 400), (2500, 7), (5000, 3)):
+        c = case(T, T, 520, 130, 24, n, torch.float16, torch.float16)
+        y0 = c["y"].clone()
+        y = ops.lora_add(**c)
+        size = ops.lib().lora_add_workspace_bytes(T, 520, 24, n)
+        ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+        rc = ops.lib().lora_add(y0.data_ptr(), 130, 1, c["x"].data_ptr(), 520, 1, c["a"].data_ptr(), c["b"].data_ptr(),
+                                c["index"].data_ptr(), c["scale"].data_ptr(), T, 130, 520, 24, n, ws.data_ptr(), size,
+                                torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and torch.equal(y0, y) and (ws[size:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("T", [4095, 4096, 4097, 9000])
+def test_more_rows_than_a_block(T):
+    check(case(T, T, 40, 33, 8, 6, torch.bfloat16, torch.float32))
+    c = case(T, T, 40, 33, 8, 6, torch.bfloat16, torch.bfloat16)
+    c["index"][:] = 4                  # one adapter for all
+    check(c)
+    c["index"][:] = torch.arange(T, device="cuda") * 7 // T - 1   # spans, the first without one
+    check(c)
+
+
+def test_as_many_adapters_as_there_may_be():
+    c = case(9, 5000, 16, 20, 8, 4096, torch.bfloat16, torch.bfloat16)
+    check(c)
+    c = case(10, 60, 16, 20, 8, 4096, torch.bfloat16, torch.bfloat16)
+    check(c)
+
+
+def test_two_captured_graphs_replayed_at_once():
+    """Each graph has its own scratch memory: replays on two streams do not meet in it."""
+    cases = [case(30 + i, 600, 2048, 1024, 32, 6, torch.bfloat16, torch.bfloat16) for i in range(2)]
+    start = [c["y"].clone() for c in cases]
+    want = [ops.lora_add(**dict(c, y=y.clone())) for c, y in zip(cases, start)]
+    torch.cuda.synchronize()
+    graphs = []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ops.lora_add(**c)
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for c, y in zip(cases, start):
+            c["y"].copy_(y)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(cases[0]["y"], want[0]) and torch.equal(cases[1]["y"], want[1])

@@ -198,3 +198,53 @@ def test_route_strides_and_given_outputs():
     rw, rids = picked.route(logits.cpu(), 4, None, "softmax", True, 1.0)
     assert w is out[0] and ids is out[1] and torch.equal(ids.cpu(), rids)
     assert ((w.cpu().double() - rw).abs() <= 2.0 ** -24 * (1 + 1e-6) * rw).all()
+
+
+def test_workspace_contents_do_not_matter_and_its_end_is_kept():
+    """The C call with a workspace of NaNs, and bytes behind it that stay."""
+    for T, H, I, E, k in ((1, 512, 256, 8, 2), (20, 288, 96, 30, 5), (70, 288, 96, 3, 2)):
+        x, ids, weights, w13, w2 = layer(11, T, H, I, E, k)
+        ids[0, 0] = -1
+        p13, p2 = ops.pack_experts(*w13), ops.pack_experts(*w2)
+        y = ops.moe_a16w4(x, ids, weights, p13, p2, I)
+        n = ops.lib().moe_a16w4_workspace_bytes(T, k, H, I)
+        ws = torch.full((n + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+        z = torch.full((T + 1, H), 7.0, device="cuda").bfloat16()
+        rc = ops.lib().moe_a16w4(x.data_ptr(), H, ids.data_ptr(), weights.data_ptr(), p13.data_ptr(), p13.stride(0),
+                                 p2.data_ptr(), p2.stride(0), z.data_ptr(), H, T, k, E, H, I, ws.data_ptr(), n,
+                                 torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and torch.equal(z[:T], y) and (z[T] == 7).all() and (ws[n:] == 0xFF).all()
+
+
+def test_two_captured_graphs_replayed_at_once():
+    """Each graph has its own scratch memory: replays on two streams do not meet in it."""
+    cases = [layer(20 + i, 70, 2048, 1024, 6, 2) for i in range(2)]
+    packed = [(ops.pack_experts(*c[3]), ops.pack_experts(*c[4])) for c in cases]
+    want = [ops.moe_a16w4(*c[:3], *p, 1024) for c, p in zip(cases, packed)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c, p in zip(cases, packed):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ops.moe_a16w4(*c[:3], *p, 1024))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_skewed_choice():
+    """Most tokens take the same expert: more rows for it than go together, few or none for the others."""
+    for T, E in ((64, 64), (200, 16), (300, 20)):
+        x, ids, weights, w13, w2 = layer(T, T, 160, 96, E, 4)
+        ids[:, 0] = E - 1
+        ids[: T // 2, 1] = 2
+        ids[ids == 5] = -1
+        check(x, ids, weights, w13, w2)

@@ -67,7 +67,7 @@ L = dict(y=P, ldy=48, yt=0, x=P, ldx=64, xt=0, a=P, b=P, index=P, scale=None, T=
 @pytest.mark.parametrize("change,status", [
     (dict(y=None), 1), (dict(x=None), 1), (dict(a=None), 1), (dict(b=None), 1), (dict(index=None), 1),
     (dict(xt=2), 8), (dict(xt=-1), 8), (dict(yt=1), 8), (dict(yt=3), 8), (dict(xt=1, yt=0), 8),
-    (dict(T=0), 2), (dict(N=0), 2), (dict(n=0), 2), (dict(T=(1 << 20) + 1), 2), (dict(n=(1 << 20) + 1), 2),
+    (dict(T=0), 2), (dict(N=0), 2), (dict(n=0), 2), (dict(T=(1 << 20) + 1), 2), (dict(n=4097), 2),
     (dict(N=(1 << 20) + 1, ldy=1 << 21), 2), (dict(K=0), 2), (dict(K=4), 2), (dict(K=60), 2),
     (dict(K=(1 << 20) + 8, ldx=1 << 21), 2), (dict(R=0), 2), (dict(R=12), 2), (dict(R=136), 2), (dict(ldx=56), 2),
     (dict(ldy=47), 2), (dict(ldx=(1 << 36) + 8), 2), (dict(ldy=(1 << 36) + 1), 2), (dict(ldx=-64), 2),
@@ -81,11 +81,12 @@ def test_lora_add_refusals(change, status):
                               a["T"], a["N"], a["K"], a["R"], a["n"], a["ws"], a["nbytes"], None) == status
 
 
-@pytest.mark.parametrize("T,K,R", [(0, 64, 16), (1, 0, 16), (1, 60, 16), (1, 64, 0), (1, 64, 12), (1, 64, 136),
-                                   (1 << 21, 64, 16), (1, 1 << 21, 16)])
-def test_lora_workspace_of_a_rejected_shape(T, K, R):
-    assert ops.lib().lora_add_workspace_bytes(T, K, R) == 0
-    assert ops.lib().lora_add_workspace_bytes(1, 64, 16) > 0
+@pytest.mark.parametrize("T,K,R,n", [(0, 64, 16, 1), (1, 0, 16, 1), (1, 60, 16, 1), (1, 64, 0, 1), (1, 64, 12, 1),
+                                     (1, 64, 136, 1), (1 << 21, 64, 16, 1), (1, 1 << 21, 16, 1), (1, 64, 16, 0),
+                                     (1, 64, 16, 4097)])
+def test_lora_workspace_of_a_rejected_shape(T, K, R, n):
+    assert ops.lib().lora_add_workspace_bytes(T, K, R, n) == 0
+    assert ops.lib().lora_add_workspace_bytes(1, 64, 16, 1) > 0
 
 
 def test_binding_refuses_what_it_cannot_marshal():
