@@ -48,21 +48,20 @@ __device__ __forceinline__ Packed packed(const uint8_t* base, int N, int K) {
   return p;
 }
 
-// The pairs (t, j) of a slot's expert. A launch has a slot for each expert that could be
-// taken: for each pair (up to 64 pairs), else for each expert where there are as many pairs as
-// experts (slot_is_expert: the expert is known at once), else for as many experts as there are
-// pairs. `list` has the slot's pairs in an order that the ids alone decide. Returns their
+// The pairs (t, j) of a slot's expert. A launch has a slot for each expert (slot_is_expert: it is
+// known at once) or, where there are fewer pairs, for each pair: then a slot stands for its own
+// pair's expert (up to 64 pairs) or for the slot-th of the experts that are taken. `list` has the slot's pairs in an order that the ids alone decide. Returns their
 // number, 0 for a slot to skip.
 struct Rows {
   uint32_t bits[kMaxE / 32];
   int count[kWaves];
   uint16_t list[MXFP4_MOE_MAX_PAIRS];
 };
-__device__ __forceinline__ bool slot_is_expert(const MoeArgs& a) { return a.T * a.k > 64 && a.T * a.k >= a.E; }
+__device__ __forceinline__ bool slot_is_expert(const MoeArgs& a) { return a.T * a.k >= a.E; }
 __device__ __forceinline__ int find_rows(const MoeArgs& a, int slot, Rows& s, int& expert) {
   const int tid = threadIdx.x, l = tid & 63, P = a.T * a.k;
-  if (P <= 64) {
-    // A slot for each pair, which goes on if it is the first with its expert.
+  if (P <= 64 && !slot_is_expert(a)) {
+    // It goes on if its pair is the first with the expert.
     const int id = l < P ? a.ids[l] : -1;
     expert = __builtin_amdgcn_readlane(id, slot);
     const uint64_t mine = __ballot(id == expert);
@@ -423,15 +422,19 @@ __global__ __launch_bounds__(kThreads) void many_kernel(MoeArgs a) {
   }
 }
 
-// y[t] = sum over the token's pairs, in their order.
+// y[t] = sum over the token's pairs, in their order. What lies in the place of a pair without an
+// expert is read like the others, at the same time as the ids, and left out.
 __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
   const int t = blockIdx.y, col = 4 * (blockIdx.x * 256 + threadIdx.x);
   if (col >= a.H) return;
   mx::v4f v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
   for (int j = 0; j < a.k; ++j) {
     const int64_t p = (int64_t)t * a.k + j;
-    if ((uint32_t)a.ids[p] < (uint32_t)a.E) v = v + *reinterpret_cast<const mx::v4f*>(a.part + p * a.H + col);
+    const bool there = (uint32_t)a.ids[p] < (uint32_t)a.E;
+    const mx::v4f q = *reinterpret_cast<const mx::v4f*>(a.part + p * a.H + col);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = v[e] + (there ? q[e] : 0.0f);
   }
   *reinterpret_cast<u32x2*>(a.y + t * a.ldy + 2 * col) = u32x2{mx::pack_bf16x2(v[0], v[1]), mx::pack_bf16x2(v[2], v[3])};
 }
@@ -598,8 +601,11 @@ extern "C" int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const f
   void* args[] = {&a};
   const hipStream_t st = (hipStream_t)stream;
   const int64_t P = T * k;
-  const bool many = P > 10 * E;  // rows to an expert
-  const unsigned slots = (unsigned)(P <= 64 || P < E ? P : E), tiles = (unsigned)(I / 32);
+  // Rows to an expert: with 10 on average the two take the same time (H 2048, I 1024, 32 experts:
+  // gate and up 18.1 and 17.5 us), with 8 few is faster (H 4096, I 1536, 16 experts: 22.5 and
+  // 25.0), with 16 many (35.8 and 29.0: few goes over the weight again for every 16 rows).
+  const bool many = P > 10 * E;
+  const unsigned slots = (unsigned)(P < E ? P : E), tiles = (unsigned)(I / 32);
   hipError_t e = many ? launch_many<true, 4>(a, slots, st)
                       : hipLaunchKernel((const void*)few_kernel, dim3(tiles, slots), dim3(kThreads), args, 0, st);
   if (e != hipSuccess) return MXFP4_ERR_HIP;
