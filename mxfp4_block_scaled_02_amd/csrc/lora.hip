@@ -6,6 +6,17 @@
 // take units of up to 64 rows with the same adapter, wherever they lie among the rows, in 16-row
 // tiles: A and B are read once for a unit, and no row meets another one's adapter. The units of
 // up to 64 rows are found by every wave itself; of more by a launch in front (plan).
+//
+// Measured on the MI355X (bf16; a copy of memory reaches 5.2 TB/s):
+//   T    K    N    R   n   us for the launches   what bounds it
+//   1    7168 2112 16  8   3.6 + 4.8             latency (a call takes 11 us on the host)
+//   64   7168 4096 32  24  6.7 + 5.2             latency: 12 and 7 MB
+//   777  2064 2113 24  5   3.3 + 4.9 + 7.3       latency (x fp16, y fp32)
+//   4096 7168 4096 64  8   5.2 + 16.5 + 21.4     x once at 3.6 TB/s; y in and out at 3.1, beside the
+//                                                partial sums, which 16 workgroups add up each
+//   4096 4096 4096 32  28  13.7 + 12.9 + 18.1    the same (adapters in any order of rows)
+#include <type_traits>
+
 #include "host_common.hpp"
 #include "mx_device.hpp"
 
@@ -40,7 +51,6 @@ struct LoraArgs {
   const float* scale;
   float* part;
   int T, N, K, R, n;
-  int unit;           // 16-row tiles that a workgroup of expand takes together
   struct Unit* units;
   int slots;          // units that a block may have
   int splits, slice;  // workgroups that share K, steps of kStage to each
@@ -84,7 +94,12 @@ __host__ __device__ inline int64_t slots_of(int64_t T, int64_t n) {
 
 // The units of a block of rows, by rising adapter, the rows of each in an order that the indices
 // alone decide: a counting sort. A wave counts the adapters of its rows (every 16th run of 64),
-// the counts are added up over the waves, and over the adapters the units. TIMES
+// the counts are added up over the waves, and over the adapters the units. A round of a wave takes
+// one adapter of its rows, and the rounds bound it: 777 rows in 5 spans 3.3 us (3.7 with room for
+// 4096), 900 rows of 16 adapters at random 5.1 (7.8), 2000 of 28 8.2 (12.3), 4096 of 28 13.7, in 8
+// spans 5.2. Past 64 rows it pays: 64 rows of 24 adapters, K 7168, N 4096, take 6.7 + 5.2 us
+// without it and 4.8 + 6.0 + 6.5 with it; each row of the other way is a workgroup that looks
+// through all rows.
 constexpr int kPlanWaves = 16;
 template <int kWords>  // runs of 64 rows to a wave
 __global__ __launch_bounds__(64 * kPlanWaves) void plan_kernel(LoraArgs a) {
@@ -313,6 +328,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(LoraArgs a) {
       const int row = row0 + __shfl(order, min(t, count - 1), 64), rank = 16 * r + 4 * g;
       if (t < count && rank < a.R) *reinterpret_cast<mx::v4f*>(a.part + ((int64_t)q * a.T + row) * a.R + rank) = v;
     };
+    // 24 rows of 6 adapters, K 4096: 3.6 us, 4.4 if all went through LDS; 64 of 24, K 7168: 6.7 and 8.1.
     if (count > 16) {
       shrink_tile<DT, RT>(a, adapter, row0, order, count, begin, end, sm.tile, acc);
 #pragma unroll
@@ -480,7 +496,8 @@ struct Columns {
     }
   }
   template <bool FULL>
-  __device__ __forceinline__ void add(const LoraArgs& a, const ExpandSmem<DT, YT, RS>& sm, int n0, int count, float scale) {
+  __device__ __forceinline__ void add(const LoraArgs& a, const ExpandSmem<DT, YT, RS>& sm, int n0, int count,
+                                      float scale) {
     const int l = threadIdx.x & 63, c = l & 15, g = l >> 4;
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) {
@@ -510,7 +527,8 @@ struct Columns {
 };
 
 template <int DT, int YT, int RS, bool FEW>
-__global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F32) ? 2 : 3) void expand_kernel(LoraArgs a) {
+__global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F32) ? 2 : 3) void expand_kernel(
+    LoraArgs a) {
   typedef typename Half<DT>::V V;
   constexpr int kPieces = YT == MXFP4_TYPE_F32 ? 3 : 2;
   constexpr int kTiles = expand_tiles<YT, RS>();
@@ -518,7 +536,7 @@ __global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = kCols * blockIdx.x + 64 * wave;
-  with_unit<FEW>(a, 16 * a.unit, [&](int adapter, int row0, int order, int count) {
+  with_unit<FEW>(a, 16 * kTiles, [&](int adapter, int row0, int order, int count) {
     const float scale = a.scale ? a.scale[adapter] : 1.0f;
     __syncthreads();
     // 8 ranks of a row to kAdders neighbouring threads, which share the partial sums; 4 RS such
@@ -555,7 +573,8 @@ __global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F
           for (int d = kAdders; d < 4 * RS * kAdders; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
           const int up = top == 0 || top >= 0x7f800000u ? 0 : min(14 + 127 - (int)(top >> 23), 126);
           const float by = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
-          if (at == 0 && i % kAdders == 0 && t < count) sm.back[t] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
+          if (at == 0 && i % kAdders == 0 && t < count)
+            sm.back[t] = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] *= by;
         }
@@ -572,6 +591,8 @@ __global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F
           }
       }
     };
+    // One thread for a row's 8 ranks is less work, several shorten the chain of loads: one row, 56 splits
+    // 8.6 us with one thread, 4.8 with 8; 4096 rows, 4 splits 21.4 and 35.6.
     if (a.splits > 12)
       sums(std::integral_constant<int, (RS == 4 ? 4 : 8)>());  // a row's threads are of one wave
     else
@@ -597,7 +618,9 @@ bool shape_ok(int64_t T, int64_t K, int64_t R, int64_t n) {
 }
 // Workgroups that share K: enough to occupy the chip, each wave one step of 32 at least; from 65
 // rows on at most 10, as every workgroup of expand adds up their sums (777 rows, K 2064, N 2113,
-// R 24: 17 splits 6.4 + 10.0 us for the two kernels, 9 splits 5.2 + 8.8).
+// R 24: 17 splits 6.4 + 10.0 us for the two kernels, 9 splits 5.2 + 8.8). Half and double as many:
+// 64 rows of 24 adapters, K 7168, 6.7 + 5.2 us against 8.0 + 4.9 and 9.3 + 6.2; 4096 rows, K 7168,
+// R 64, 16.0 + 21.2 against 23.3 + 20.2 and 17.5 + 24.9.
 int splits_of(int64_t T, int64_t K) {
   const int64_t stages = mxh::cdiv(K, kStage), most = mxh::cdiv(stages, 2);
   const int64_t want = T <= kFew ? mxh::cdiv(512, T < 32 ? T : 32) : T < 26 * 64 ? 10 : mxh::cdiv(16384, T);
@@ -612,15 +635,17 @@ dim3 grid_of(const LoraArgs& a, unsigned x, int rows) {
 template <int DT, int RT, int U>
 hipError_t launch_shrink(LoraArgs& a, hipStream_t st) {
   void* args[] = {&a};
-  return hipLaunchKernel(a.T <= kFew ? (const void*)shrink_kernel<DT, RT, U, true> : (const void*)shrink_kernel<DT, RT, U, false>,
-                         grid_of(a, (unsigned)a.splits, kUnit), dim3(kThreads), args, 0, st);
+  const void* f =
+      a.T <= kFew ? (const void*)shrink_kernel<DT, RT, U, true> : (const void*)shrink_kernel<DT, RT, U, false>;
+  return hipLaunchKernel(f, grid_of(a, (unsigned)a.splits, kUnit), dim3(kThreads), args, 0, st);
 }
 template <int DT, int YT, int RS>
 hipError_t launch_expand(LoraArgs& a, hipStream_t st) {
-  a.unit = a.T <= 2048 ? 1 : expand_tiles<YT, RS>();
   void* args[] = {&a};
-  return hipLaunchKernel(a.T <= kFew ? (const void*)expand_kernel<DT, YT, RS, true> : (const void*)expand_kernel<DT, YT, RS, false>,
-                         grid_of(a, (unsigned)mxh::cdiv(a.N, kCols), 16 * a.unit), dim3(kThreads), args, 0, st);
+  const void* f =
+      a.T <= kFew ? (const void*)expand_kernel<DT, YT, RS, true> : (const void*)expand_kernel<DT, YT, RS, false>;
+  return hipLaunchKernel(f, grid_of(a, (unsigned)mxh::cdiv(a.N, kCols), 16 * expand_tiles<YT, RS>()), dim3(kThreads),
+                         args, 0, st);
 }
 size_t part_bytes(int64_t T, int64_t K, int64_t R) { return (size_t)splits_of(T, K) * (size_t)T * (size_t)R * 4; }
 
@@ -669,9 +694,10 @@ extern "C" int lora_add(void* y, int64_t ldy, int ytype, const void* x, int64_t 
   if (!workspace || !mxh::aligned(workspace, 16) || workspace_bytes < lora_add_workspace_bytes(T, K, R, n))
     return MXFP4_ERR_WORKSPACE;
   const int splits = splits_of(T, K);
-  LoraArgs p{(uint8_t*)y, ldy,   (const uint8_t*)x, ldx * 2, (const uint8_t*)a, (const uint8_t*)b, index, scale,
+  LoraArgs p{(uint8_t*)y, ldy, (const uint8_t*)x, ldx * 2, (const uint8_t*)a, (const uint8_t*)b, index, scale,
              (float*)workspace, (int)T, (int)N, (int)K, (int)R, (int)n,
-             0, (Unit*)((uint8_t*)workspace + part_bytes(T, K, R)), (int)slots_of(T, n), splits, (int)mxh::cdiv(mxh::cdiv(K, kStage), splits)};
+             (Unit*)((uint8_t*)workspace + part_bytes(T, K, R)), (int)slots_of(T, n), splits,
+             (int)mxh::cdiv(mxh::cdiv(K, kStage), splits)};
   const hipStream_t st = (hipStream_t)stream;
   if (xtype == MXFP4_TYPE_BF16)
     return ytype == MXFP4_TYPE_F32 ? launch<MXFP4_TYPE_BF16, MXFP4_TYPE_F32>(p, st)

@@ -1,9 +1,24 @@
 // moe_a16w4: the experts' gated MLP of a mixture of experts on MXFP4 weights for a few
 // tokens (bf16 activations; the weights' bytes bound it, so the activations are not
 // quantised).
+//
+// Two or three launches: gate, up and SwiGLU into h; the down product; where a token's experts
+// are not added up in that product (tokens_kernel), their sum (combine_kernel). A workgroup has
+// some columns of one expert, finds the rows that take it in `ids` by itself, and reads its part of
+// the weight once for up to 16 (few_kernel) or 64 (many_kernel) of them: no launch sorts the rows,
+// and nothing goes back to the host.
+//
+// Measured on the MI355X (a linear read of memory reaches 5.5 to 5.8 TB/s, a copy 5.2):
+//   T   k  E   H    I     us for the launches    what bounds it
+//   1   8  32  7168 2048  21.6 + 15.2            the weights of 8 experts, 187 MB: 5.8 and 4.1 TB/s
+//   64  8  64  7168 2048  181 + 96.7 + 4.9       all weights, 1.50 GB: 5.5 and 5.2 TB/s
+//   37  3  24  2112 1056  16 + 11.2 + 4          latency: one pass of 33 and 17 workgroups an expert
+//   256 4  32  2048 1024  22.9 + 20.3 + 4.6      the FP4 conversions and products, about 14 us each
+//   2   2  8   512  256   4.2 + 4.7              latency (a call takes 11 us on the host)
 #include "host_common.hpp"
 #include "mx_device.hpp"
 
+// Sums in the order that the code gives them, whichever variant computes a row.
 #pragma clang fp contract(off)
 
 namespace {
@@ -50,8 +65,10 @@ __device__ __forceinline__ Packed packed(const uint8_t* base, int N, int K) {
 
 // The pairs (t, j) of a slot's expert. A launch has a slot for each expert (slot_is_expert: it is
 // known at once) or, where there are fewer pairs, for each pair: then a slot stands for its own
-// pair's expert (up to 64 pairs) or for the slot-th of the experts that are taken. `list` has the slot's pairs in an order that the ids alone decide. Returns their
-// number, 0 for a slot to skip.
+// pair's expert (up to 64 pairs: one ballot, no pass over LDS; 2 tokens, k 2, E 8, H 512: 4.2 us
+// for the launch and 5.7 without, one token, k 8, H 7168: 21.6 and 23.1) or for the slot-th of the
+// experts that are taken. `list` has the slot's pairs in an order that the ids alone decide.
+// Returns their number, 0 for a slot to skip.
 struct Rows {
   uint32_t bits[kMaxE / 32];
   int count[kWaves];
@@ -165,7 +182,8 @@ __device__ __forceinline__ void load_codes(const Tile* t, int step, Codes<NC>& c
 #pragma unroll
   for (int i = 0; i < NC; ++i)
     c.w[i] = __builtin_amdgcn_raw_buffer_load_b128(
-        t[SPLIT ? i : i / 2].units, 2048 * step + 1024 * (g >> 1) + 16 * (lane + 16 * (SPLIT ? h : i & 1)), 0, kNonTemporal);
+        t[SPLIT ? i : i / 2].units, 2048 * step + 1024 * (g >> 1) + 16 * (lane + 16 * (SPLIT ? h : i & 1)), 0,
+        kNonTemporal);
 }
 // acc[r][i] += rows 16 r .. times column group i over a step; f(r, pl, j): the lane's elements
 // 8 j .. 8 j + 7 of its row of tile r, of the row's PL parts whose sum it is.
@@ -215,7 +233,8 @@ __device__ __forceinline__ void clear(mx::v4f (&acc)[NT][NC]) {
 
 // h of a pair is kept as two bf16 parts, the value's rounding and the rest's (within 2^-17 of it
 // together): one part alone would put an error into y as large as y's own rounding. The second
-// part costs a matrix instruction more, where the bytes of the weights set the time.
+// part costs a matrix instruction more (256 tokens, k 4, 32 experts, H 2048, I 1024: 48.6 us for the
+// call with one, 49.3 with both).
 __device__ __forceinline__ const uint8_t* h_row(const MoeArgs& a, int part, int pair) {
   return a.h + ((int64_t)part * a.T * a.k + pair) * a.I * 2;
 }
@@ -309,7 +328,8 @@ struct Columns {
   Tile t[2];
   int unit, units, half;
   __device__ __forceinline__ Columns(const MoeArgs& a, int expert) {
-    const Packed p = UP ? packed(a.w13 + expert * a.stride13, 2 * a.I, a.H) : packed(a.w2 + expert * a.stride2, a.H, a.I);
+    const Packed p =
+        UP ? packed(a.w13 + expert * a.stride13, 2 * a.I, a.H) : packed(a.w2 + expert * a.stride2, a.H, a.I);
     unit = kWaves * blockIdx.x + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     units = UP ? a.I / (8 * NC) : (a.H + 16 * NC - 1) / (16 * NC);
     const int u = min(unit, units - 1), t0 = UP ? u * NC / 4 : u * NC / 2;
@@ -317,7 +337,9 @@ struct Columns {
     t[0] = tile_at(p, t0);
     t[1] = tile_at(p, UP ? a.I / 32 + t0 : min(t0 + 1, a.H / 32 - 1));
   }
-  __device__ __forceinline__ void load(int step, Codes<NC>& c) const { load_codes<NC, UP && NC == 2>(t, step, c, half); }
+  __device__ __forceinline__ void load(int step, Codes<NC>& c) const {
+    load_codes<NC, UP && NC == 2>(t, step, c, half);
+  }
 };
 template <bool UP, int NT, int NC, typename SMEM>
 __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC>& o, int first, int n, SMEM& sm,
@@ -378,7 +400,8 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC
     const int pair = sm.rows.list[at];
     if constexpr (UP) {
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) store_h(a, pair, 8 * NC * o.unit + 16 * i + 4 * g, acc[r][i], acc[r][NC / 2 + i]);
+      for (int i = 0; i < NC / 2; ++i)
+        store_h(a, pair, 8 * NC * o.unit + 16 * i + 4 * g, acc[r][i], acc[r][NC / 2 + i]);
     } else {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -436,34 +459,43 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = v[e] + (there ? q[e] : 0.0f);
   }
-  *reinterpret_cast<u32x2*>(a.y + t * a.ldy + 2 * col) = u32x2{mx::pack_bf16x2(v[0], v[1]), mx::pack_bf16x2(v[2], v[3])};
+  *reinterpret_cast<u32x2*>(a.y + t * a.ldy + 2 * col) =
+      u32x2{mx::pack_bf16x2(v[0], v[1]), mx::pack_bf16x2(v[2], v[3])};
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: the down product over all their experts, 32 columns to a workgroup
+// Few tokens: the down product over all their experts, 32 or 16 columns to a workgroup
 // ---------------------------------------------------------------------------
 // The rows are the tokens, so that the sum over a token's experts is the matrix instruction's
 // own: no partial products in memory, no launch to add them. The work is a list of (expert,
 // 128 k), taken in turn by the waves; h of all pairs lies in LDS, piece p (8 k) of a row of
 // token t at p ^ t, which spreads a piece of the tokens over distinct banks. A token without the
-// expert has a row of zeros.
+// expert has a row of zeros. Against many_kernel and combine_kernel: one token, k 8, H 7168, I 2048
+// 15.2 us and 15.3 + 4.4; 2 tokens, k 2, H 512, I 256 4.7 and 4.2 + 1.7; 8 tokens, k 8, H 4096,
+// I 256 17.8 and 12.9 + 3.9; beside a launch less.
 constexpr int kTokens = 16, kTokenPairs = 64;
 constexpr int kTokenPieces = 2048;  // of 8 k: all pairs' I, each rounded up to 128
 constexpr int kTokenWaves = 16;
+template <int NC>
 struct TokenSmem {
+  int slots;
   u32x4 h[2][kTokenPieces];
   u32x4 zero;
   int expert[kTokenPairs];             // of a slot
   int16_t pair[kTokenPairs][kTokens];  // of a slot's token, -1 without one
-  mx::v4f red[kTokenWaves][2][64];
+  mx::v4f red[kTokenWaves][NC][64];
 };
 // Slots are the distinct (expert, turn) in the order of their first pairs; a pair's turn is how
-// often its token has its expert before. Lane p of every wave has pair p. Returns their number.
-__device__ __forceinline__ int find_slots(const MoeArgs& a, TokenSmem& s) {
+// often its token has its expert before. One wave finds them: lane p has pair p.
+template <int NC>
+__device__ __forceinline__ void find_slots(const MoeArgs& a, TokenSmem<NC>& s) {
   const int tid = threadIdx.x, l = tid & 63, P = a.T * a.k;
   const int id = l < P ? a.ids[l] : -1, token = l / a.k;
+  for (int i = tid; i < kTokenPairs * kTokens / 2; i += 64 * kTokenWaves)
+    reinterpret_cast<uint32_t*>(s.pair)[i] = ~0u;
+  __syncthreads();
+  if (tid >= 64) return;
   const bool there = (uint32_t)id < (uint32_t)a.E;
-  for (int i = tid; i < kTokenPairs * kTokens / 2; i += 64 * kTokenWaves) reinterpret_cast<uint32_t*>(s.pair)[i] = ~0u;
   int lead = l;  // one token: every pair is a slot of its own
   if (a.T > 1) {
     int turn = 0;
@@ -473,16 +505,16 @@ __device__ __forceinline__ int find_slots(const MoeArgs& a, TokenSmem& s) {
   }
   const uint64_t leads = __ballot(there && lead == l);
   const int slot = __popcll(leads & (((uint64_t)1 << lead) - 1));
-  __syncthreads();
-  if (tid < 64 && there) {
+  if (there) {
     if (lead == l) s.expert[slot] = id;
     s.pair[slot][token] = (int16_t)l;
   }
-  __syncthreads();
-  return __popcll(leads);
+  if (l == 0) s.slots = __popcll(leads);
 }
+// 16 NC columns to a workgroup.
+template <int NC>
 __global__ __launch_bounds__(64 * kTokenWaves) void tokens_kernel(MoeArgs a) {
-  __shared__ __align__(16) TokenSmem sm;
+  __shared__ __align__(16) TokenSmem<NC> sm;
   const int tid = threadIdx.x, l = tid & 63, c = l & 15, g = l >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int P = a.T * a.k, steps = (a.I + 127) / 128, pieces = 16 * steps;  // of a row
@@ -510,25 +542,26 @@ __global__ __launch_bounds__(64 * kTokenWaves) void tokens_kernel(MoeArgs a) {
     }
   }
   if (tid == 0) sm.zero = u32x4{0, 0, 0, 0};
-  const int slots = find_slots(a, sm);
+  find_slots(a, sm);
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
 #pragma unroll
     for (int pl = 0; pl < 2; ++pl)
       if (at[i] >= 0) sm.h[pl][at[i]] = held[pl][i];
   __syncthreads();
-  mx::v4f acc[1][2];
+  const int slots = sm.slots;
+  mx::v4f acc[1][NC];
   clear(acc);
   int slot = wave / steps, s = wave - slot * steps;
   const int by = kTokenWaves / steps, rest = kTokenWaves - by * steps;
 #pragma unroll 1
   while (slot < slots) {
     const Packed p = packed(a.w2 + __builtin_amdgcn_readfirstlane(sm.expert[slot]) * a.stride2, a.H, a.I);
-    const Tile t[1] = {tile_at(p, blockIdx.x)};
-    Codes<2> code;
-    load_codes<2>(t, s, code);
+    const Tile t[1] = {tile_at(p, NC == 2 ? blockIdx.x : blockIdx.x / 2)};
+    Codes<NC> code;
+    load_codes<NC, NC == 1>(t, s, code, blockIdx.x & 1);
     const int pair = sm.pair[slot][c];
-    multiply<1, 2, 2>(code, s, [&](int, int pl, int j) {
+    multiply<1, 2, NC>(code, s, [&](int, int pl, int j) {
       const u32x4* x = pair >= 0 ? &sm.h[pl][pair * pieces + ((16 * s + 4 * g + j) ^ c)] : &sm.zero;
       return __builtin_bit_cast(v8bf, *x);
     }, acc);
@@ -540,13 +573,13 @@ __global__ __launch_bounds__(64 * kTokenWaves) void tokens_kernel(MoeArgs a) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) sm.red[wave][i][l] = acc[0][i];
+  for (int i = 0; i < NC; ++i) sm.red[wave][i][l] = acc[0][i];
   __syncthreads();
-  if (wave >= 2 || c >= a.T) return;
+  if (wave >= NC || c >= a.T) return;
   mx::v4f y = sm.red[0][wave][l];
 #pragma unroll
   for (int w = 1; w < kTokenWaves; ++w) y = y + sm.red[w][wave][l];
-  *reinterpret_cast<u32x2*>(a.y + c * a.ldy + 2 * (32 * (int)blockIdx.x + 16 * wave + 4 * g)) =
+  *reinterpret_cast<u32x2*>(a.y + c * a.ldy + 2 * (16 * NC * (int)blockIdx.x + 16 * wave + 4 * g)) =
       u32x2{mx::pack_bf16x2(y[0], y[1]), mx::pack_bf16x2(y[2], y[3])};
 }
 
@@ -556,12 +589,12 @@ __global__ __launch_bounds__(64 * kTokenWaves) void tokens_kernel(MoeArgs a) {
 template <bool UP, int MAXNT>
 hipError_t launch_many(MoeArgs& a, unsigned slots, hipStream_t st) {
   void* args[] = {&a};
-  const unsigned units = (unsigned)mxh::cdiv(UP ? a.I : a.H, UP ? 32 * kWaves : 64 * kWaves);
-  if (units * slots >= 600)
-    return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 4>, dim3(units, slots), dim3(kThreads), args, 0, st);
-  return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 2>,
-                         dim3((unsigned)mxh::cdiv(UP ? a.I : a.H, UP ? 16 * kWaves : 32 * kWaves), slots), dim3(kThreads),
-                         args, 0, st);
+  const int64_t columns = UP ? a.I : a.H;
+  const unsigned wide = (unsigned)mxh::cdiv(columns, UP ? 32 * kWaves : 64 * kWaves);
+  if (wide * slots >= 600)
+    return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 4>, dim3(wide, slots), dim3(kThreads), args, 0, st);
+  const unsigned narrow = (unsigned)mxh::cdiv(columns, UP ? 16 * kWaves : 32 * kWaves);
+  return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 2>, dim3(narrow, slots), dim3(kThreads), args, 0, st);
 }
 
 bool shape_ok(int64_t T, int64_t k, int64_t H, int64_t I) {
@@ -609,11 +642,17 @@ extern "C" int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const f
   hipError_t e = many ? launch_many<true, 4>(a, slots, st)
                       : hipLaunchKernel((const void*)few_kernel, dim3(tiles, slots), dim3(kThreads), args, 0, st);
   if (e != hipSuccess) return MXFP4_ERR_HIP;
-  if (T <= kTokens && P <= kTokenPairs && P * mxh::cdiv(I, 128) * 16 <= kTokenPieces)
-    return mxh::launch_status(hipLaunchKernel((const void*)tokens_kernel, dim3((unsigned)(H / 32)),
-                                              dim3(64 * kTokenWaves), args, 0, st));
+  if (T <= kTokens && P <= kTokenPairs && P * mxh::cdiv(I, 128) * 16 <= kTokenPieces) {
+    // 16 columns to a workgroup while there is a CU for each (4 tokens, k 4, H 4096, I 1024: 256
+    // workgroups 13.2 us, 128 of 32 columns 14.6), else 32: LDS lets one workgroup to a CU (one
+    // token, k 8, H 7168, I 2048: 448 workgroups 24.3 us, 224 of 32 columns 15.2).
+    const bool narrow = H <= 16 * 256;
+    const void* f = narrow ? (const void*)tokens_kernel<1> : (const void*)tokens_kernel<2>;
+    const dim3 grid((unsigned)(narrow ? H / 16 : H / 32));
+    return mxh::launch_status(hipLaunchKernel(f, grid, dim3(64 * kTokenWaves), args, 0, st));
+  }
   e = many ? launch_many<false, 4>(a, slots, st) : launch_many<false, 1>(a, slots, st);
   if (e != hipSuccess) return MXFP4_ERR_HIP;
-  return mxh::launch_status(hipLaunchKernel((const void*)combine_kernel, dim3((unsigned)mxh::cdiv(H, 1024), (unsigned)T),
-                                            dim3(256), args, 0, st));
+  const dim3 grid((unsigned)mxh::cdiv(H, 1024), (unsigned)T);
+  return mxh::launch_status(hipLaunchKernel((const void*)combine_kernel, grid, dim3(256), args, 0, st));
 }

@@ -248,3 +248,15 @@ def test_skewed_choice():
         ids[: T // 2, 1] = 2
         ids[ids == 5] = -1
         check(x, ids, weights, w13, w2)
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(16, 4096, 128, 9, 4), (16, 4128, 128, 9, 4), (8, 4096, 160, 6, 6), (8, 4128, 160, 6, 6),
+                                       (1, 4096, 2048, 12, 8), (1, 4128, 4096, 5, 4), (17, 4128, 64, 9, 3)])
+def test_few_tokens(T, H, I, E, k):
+    """On either side of the sizes at which the down product goes another way; experts that a token takes more than once."""
+    x, ids, weights, w13, w2 = layer(T + H, T, H, I, E, k)
+    check(x, ids, weights, w13, w2)
+    ids[-1] = ids[0, 0]
+    ids[:, 1] = ids[:, 0]
+    ids[T // 2, 0] = -1
+    check(x, ids, weights, w13, w2)
