@@ -11,9 +11,10 @@
 // Measured on the MI355X (a linear read of memory reaches 5.5 to 5.8 TB/s, a copy 5.2):
 //   T   k  E   H    I     us for the launches    what bounds it
 //   1   8  32  7168 2048  21.6 + 15.2            the weights of 8 experts, 187 MB: 5.8 and 4.1 TB/s
-//   64  8  64  7168 2048  181 + 96.7 + 4.9       all weights, 1.50 GB: 5.5 and 5.2 TB/s
-//   37  3  24  2112 1056  16 + 11.2 + 4          latency: one pass of 33 and 17 workgroups an expert
-//   256 4  32  2048 1024  22.9 + 20.3 + 4.6      the FP4 conversions and products, about 14 us each
+//   64  8  64  7168 2048  181 + 98 + 4.9         all weights, 1.50 GB: 5.5 and 5.2 TB/s
+//   37  3  24  2112 1056  16.3 + 11.3 + 3.9      latency: one pass of 33 and 17 workgroups an expert
+//   124 4  6   2240 1568  42.3 + 4.6             latency: 150 and 108 workgroups for 32 rows each
+//   256 4  32  2048 1024  23 + 20.4 + 4.7        the FP4 conversions and products, about 14 us each
 //   2   2  8   512  256   4.2 + 4.7              latency (a call takes 11 us on the host)
 #include "host_common.hpp"
 #include "mx_device.hpp"
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(MoeArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// More rows to an expert, and the down product: 64 columns to a wave, activations through LDS
+// More rows to an expert, and the down product: 32 columns to a wave, activations through LDS
 // ---------------------------------------------------------------------------
 // A 128-k step of up to 64 rows lies in LDS as 16 pieces of 16 bytes to a row, piece p of row r
 // at p ^ (r % 16): the operand reads (one piece of 16 rows) and the writes (a row's pieces) hit
@@ -316,14 +317,17 @@ struct ManySmem {
   Rows rows;
   u32x4 x[2][PL][16 * MAXNT][16];
 };
-template <int NT, int PL, int NC>
+template <int NT, int PL>
 struct ManyStep {
-  Codes<NC> code;
+  Codes<2> code;
   u32x4 x[PL][NT];
 };
-// A wave's columns: 8 NC of gate and the same of up, or 16 NC of the down product. A wave past the
-// last ones repeats them and stores nothing: it still fetches its share of rows.
-template <bool UP, int NC>
+// A wave's columns: 16 of gate and of up, or 32 of the down product. A wave past the last ones repeats
+// them and stores nothing: it still fetches its share of rows. Twice as many columns to a wave
+// (half the reads of LDS) took 128 tokens, k 8, 64 experts, H 7168, I 2048 211 + 138 us against 206 + 129,
+// 256 tokens, k 8, 128 experts, H 2048, I 768 53 + 45 against 51 + 40; 512 tokens, k 8, 64 experts,
+// H 7168, I 2048 402 + 333 against 442 + 335.
+template <bool UP>
 struct Columns {
   Tile t[2];
   int unit, units, half;
@@ -331,19 +335,17 @@ struct Columns {
     const Packed p =
         UP ? packed(a.w13 + expert * a.stride13, 2 * a.I, a.H) : packed(a.w2 + expert * a.stride2, a.H, a.I);
     unit = kWaves * blockIdx.x + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    units = UP ? a.I / (8 * NC) : (a.H + 16 * NC - 1) / (16 * NC);
-    const int u = min(unit, units - 1), t0 = UP ? u * NC / 4 : u * NC / 2;
+    units = UP ? a.I / 16 : a.H / 32;
+    const int u = min(unit, units - 1);
     half = u & 1;
-    t[0] = tile_at(p, t0);
-    t[1] = tile_at(p, UP ? a.I / 32 + t0 : min(t0 + 1, a.H / 32 - 1));
+    t[0] = tile_at(p, UP ? u / 2 : u);
+    if constexpr (UP) t[1] = tile_at(p, a.I / 32 + u / 2);
   }
-  __device__ __forceinline__ void load(int step, Codes<NC>& c) const {
-    load_codes<NC, UP && NC == 2>(t, step, c, half);
-  }
+  __device__ __forceinline__ void load(int step, Codes<2>& c) const { load_codes<2, UP>(t, step, c, half); }
 };
-template <bool UP, int NT, int NC, typename SMEM>
-__device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC>& o, int first, int n, SMEM& sm,
-                                          const Codes<NC> (&begin)[2]) {
+template <bool UP, int NT, typename SMEM>
+__device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP>& o, int first, int n, SMEM& sm,
+                                          const Codes<2> (&begin)[2]) {
   constexpr int PL = UP ? 1 : 2;
   const int tid = threadIdx.x, l = tid & 63, c = l & 15, g = l >> 4;
   const int K = UP ? a.H : a.I;
@@ -355,10 +357,10 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC
 #pragma unroll
     for (int pl = 0; pl < PL; ++pl) row[pl][r] = (UP ? a.x + pair / a.k * a.ldx : h_row(a, pl, pair)) + 16 * piece;
   }
-  mx::v4f acc[NT][NC];
+  mx::v4f acc[NT][2];
   clear(acc);
   const int steps = (K + 127) / 128;
-  auto load = [&](int s, ManyStep<NT, PL, NC>& v) {
+  auto load = [&](int s, ManyStep<NT, PL>& v) {
     if (s >= 2) o.load(s, v.code);
     const int64_t at = 128 * s + 8 * piece < K ? 256 * (int64_t)s : -16 * (int64_t)piece;  // past K: the row's start
 #pragma unroll
@@ -366,13 +368,13 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC
 #pragma unroll
       for (int r = 0; r < NT; ++r) v.x[pl][r] = *reinterpret_cast<const u32x4*>(row[pl][r] + at);
   };
-  auto put = [&](const ManyStep<NT, PL, NC>& v, int buf) {
+  auto put = [&](const ManyStep<NT, PL>& v, int buf) {
 #pragma unroll
     for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
       for (int r = 0; r < NT; ++r) sm.x[buf][pl][16 * r + (tid >> 4)][piece ^ (tid >> 4)] = v.x[pl][r];
   };
-  ManyStep<NT, PL, NC> v[2];
+  ManyStep<NT, PL> v[2];
   load(0, v[0]);
   load(1, v[1]);
   v[0].code = begin[0];
@@ -383,11 +385,11 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC
     for (int i = 0; i < 2; ++i) {
       __syncthreads();
       put(v[1 - i], 1 - i);
-      const Codes<NC> code = v[i].code;
+      const Codes<2> code = v[i].code;
       load(s + i + 2, v[i]);
       __builtin_amdgcn_sched_barrier(0);  // keeps the loads ahead of the products
       if (s + i < steps)
-        multiply<NT, PL, NC>(code, i, [&](int r, int pl, int j) {
+        multiply<NT, PL, 2>(code, i, [&](int r, int pl, int j) {
           return __builtin_bit_cast(v8bf, sm.x[i][pl][16 * r + c][(4 * g + j) ^ c]);
         }, acc);
     }
@@ -399,27 +401,23 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP, NC
     if (at >= n) continue;
     const int pair = sm.rows.list[at];
     if constexpr (UP) {
-#pragma unroll
-      for (int i = 0; i < NC / 2; ++i)
-        store_h(a, pair, 8 * NC * o.unit + 16 * i + 4 * g, acc[r][i], acc[r][NC / 2 + i]);
+      store_h(a, pair, 16 * o.unit + 4 * g, acc[r][0], acc[r][1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int col = 16 * NC * o.unit + 16 * i + 4 * g;
-        if (col < a.H) *reinterpret_cast<mx::v4f*>(a.part + (int64_t)pair * a.H + col) = acc[r][i];
-      }
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<mx::v4f*>(a.part + (int64_t)pair * a.H + 32 * o.unit + 16 * i + 4 * g) = acc[r][i];
     }
   }
 }
 
-// MAXNT row tiles at most go together.
-template <bool UP, int MAXNT, int NC>
-__global__ __launch_bounds__(kThreads) void many_kernel(MoeArgs a) {
+// `tiles` <= MAXNT row tiles go together; the workgroups along z share an expert's rows.
+template <bool UP, int MAXNT>
+__global__ __launch_bounds__(kThreads) void many_kernel(MoeArgs a, int tiles) {
   __shared__ __align__(16) ManySmem<MAXNT, UP ? 1 : 2> sm;
   int expert = blockIdx.y;
-  Codes<NC> begin[2];
+  Codes<2> begin[2];
   auto start = [&]() {
-    const Columns<UP, NC> o(a, __builtin_amdgcn_readfirstlane(expert));
+    const Columns<UP> o(a, __builtin_amdgcn_readfirstlane(expert));
     o.load(0, begin[0]);
     o.load(1, begin[1]);
   };
@@ -429,19 +427,20 @@ __global__ __launch_bounds__(kThreads) void many_kernel(MoeArgs a) {
   const int n = find_rows(a, blockIdx.y, sm.rows, expert);
   if (n == 0) return;
   if (!direct) start();
-  const Columns<UP, NC> o(a, __builtin_amdgcn_readfirstlane(expert));
-  for (int first = 0; first < n; first += 16 * MAXNT) {
-    const int left = n - first;
+  const Columns<UP> o(a, __builtin_amdgcn_readfirstlane(expert));
+  const int rows = 16 * tiles, step = rows * gridDim.z;
+  for (int first = rows * blockIdx.z; first < n; first += step) {
+    const int left = min(n - first, rows);
     if (MAXNT == 1 || left <= 16)
-      many_rows<UP, 1, NC>(a, o, first, n, sm, begin);
+      many_rows<UP, 1>(a, o, first, n, sm, begin);
     else if (left <= 32)
-      many_rows<UP, MAXNT == 1 ? 1 : 2, NC>(a, o, first, n, sm, begin);
+      many_rows<UP, MAXNT == 1 ? 1 : 2>(a, o, first, n, sm, begin);
     else if (left <= 48)
-      many_rows<UP, MAXNT == 1 ? 1 : 3, NC>(a, o, first, n, sm, begin);
+      many_rows<UP, MAXNT == 1 ? 1 : 3>(a, o, first, n, sm, begin);
     else
-      many_rows<UP, MAXNT, NC>(a, o, first, n, sm, begin);
+      many_rows<UP, MAXNT>(a, o, first, n, sm, begin);
     __syncthreads();
-    if (left > 16 * MAXNT) start();
+    if (first + step < n) start();
   }
 }
 
@@ -474,7 +473,9 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
 // 15.2 us and 15.3 + 4.4; 2 tokens, k 2, H 512, I 256 4.7 and 4.2 + 1.7; 8 tokens, k 8, H 4096,
 // I 256 17.8 and 12.9 + 3.9; beside a launch less.
 constexpr int kTokens = 16, kTokenPairs = 64;
-constexpr int kTokenPieces = 2048;  // of 8 k: all pairs' I, each rounded up to 128
+// Of 8 k: all pairs' I, each rounded up to 128. With 2048 at most 5 tokens, k 2, H 3392, I 1856 took
+// 12.4 + 3.9 us in the other two launches, here 11.0; 3 tokens, k 8, H 4096, I 1024 12.0 + 3.9 and 17.5.
+constexpr int kTokenPieces = 3072;
 constexpr int kTokenWaves = 16;
 template <int NC>
 struct TokenSmem {
@@ -583,18 +584,26 @@ __global__ __launch_bounds__(64 * kTokenWaves) void tokens_kernel(MoeArgs a) {
       u32x2{mx::pack_bf16x2(y[0], y[1]), mx::pack_bf16x2(y[2], y[3])};
 }
 
-// 64 columns to a wave, or 32 where that would leave the chip short of workgroups (down product
-// of 37 tokens and 24 experts, I 1056, H 2112, 216 or 408 workgroups: 11.8 and 11.1 us; of 64
-// tokens and 64 experts, I 2048, H 7168, 1792 or 3584: 94 and 95).
+// Up to 64 rows go together, so that a weight is expanded once for them; 32 where 64 would leave the chip
+// short of workgroups (124 tokens, k 4, 6 experts, H 2240, I 1568: 42.3 us for the two launches, 47.2
+// with 64, 58.8 with 16; 512 tokens, k 8, 16 experts, H 7168, I 512 202 with 64, 223 with 32).
+// Workgroups along z for an expert's further rows, up to 512 in all and as many as one expert's rows may
+// take: those without rows end after find_rows (the same two cases: one workgroup for all of an
+// expert's rows 65 and 312 us).
 template <bool UP, int MAXNT>
 hipError_t launch_many(MoeArgs& a, unsigned slots, hipStream_t st) {
-  void* args[] = {&a};
-  const int64_t columns = UP ? a.I : a.H;
-  const unsigned wide = (unsigned)mxh::cdiv(columns, UP ? 32 * kWaves : 64 * kWaves);
-  if (wide * slots >= 600)
-    return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 4>, dim3(wide, slots), dim3(kThreads), args, 0, st);
-  const unsigned narrow = (unsigned)mxh::cdiv(columns, UP ? 16 * kWaves : 32 * kWaves);
-  return hipLaunchKernel((const void*)many_kernel<UP, MAXNT, 2>, dim3(narrow, slots), dim3(kThreads), args, 0, st);
+  const int64_t P = (int64_t)a.T * a.k;
+  const unsigned units = (unsigned)mxh::cdiv(UP ? a.I : a.H, (UP ? 16 : 32) * kWaves);
+  const int64_t groups = (int64_t)units * slots;
+  int tiles = MAXNT;
+  unsigned z = 1;
+  if (MAXNT > 1) {
+    if (groups * mxh::cdiv(P, (int64_t)slots * 16 * MAXNT) < 512) tiles = 2;
+    const int64_t most = mxh::cdiv(P, 16 * tiles), want = mxh::cdiv(512, groups);
+    z = (unsigned)(most < want ? most : want);
+  }
+  void* args[] = {&a, &tiles};
+  return hipLaunchKernel((const void*)many_kernel<UP, MAXNT>, dim3(units, slots, z), dim3(kThreads), args, 0, st);
 }
 
 bool shape_ok(int64_t T, int64_t k, int64_t H, int64_t I) {

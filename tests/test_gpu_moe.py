@@ -251,7 +251,8 @@ def test_skewed_choice():
 
 
 @pytest.mark.parametrize("T,H,I,E,k", [(16, 4096, 128, 9, 4), (16, 4128, 128, 9, 4), (8, 4096, 160, 6, 6), (8, 4128, 160, 6, 6),
-                                       (1, 4096, 2048, 12, 8), (1, 4128, 4096, 5, 4), (17, 4128, 64, 9, 3)])
+                                       (1, 4096, 2048, 12, 8), (1, 4128, 4096, 5, 4), (17, 4128, 64, 9, 3),
+                                       (3, 288, 1024, 9, 8), (3, 288, 1056, 9, 8), (1, 64, 24576, 3, 2)])
 def test_few_tokens(T, H, I, E, k):
     """On either side of the sizes at which the down product goes another way; experts that a token takes more than once."""
     x, ids, weights, w13, w2 = layer(T + H, T, H, I, E, k)
@@ -259,4 +260,17 @@ def test_few_tokens(T, H, I, E, k):
     ids[-1] = ids[0, 0]
     ids[:, 1] = ids[:, 0]
     ids[T // 2, 0] = -1
+    check(x, ids, weights, w13, w2)
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(100, 160, 96, 2, 1), (300, 96, 160, 2, 2), (700, 64, 544, 3, 2), (1000, 4096, 96, 4, 4),
+                                       (250, 96, 2080, 3, 2), (130, 2048, 2048, 2, 1), (4096, 288, 64, 9, 1)])
+def test_many_rows_to_an_expert(T, H, I, E, k):
+    """More rows of an expert than go together: several workgroups have them, or one in turns, or one expert has all."""
+    x, ids, weights, w13, w2 = layer(T + H, T, H, I, E, k)
+    check(x, ids, weights, w13, w2)
+    ids[:] = E - 1
+    ids[T // 2 :, 0] = -1
+    check(x, ids, weights, w13, w2)
+    ids[:, 0] = torch.arange(T, device="cuda") % E
     check(x, ids, weights, w13, w2)
