@@ -51,6 +51,7 @@ struct LoraArgs {
   const float* scale;
   float* part;
   int T, N, K, R, n;
+  int tiles;  // 16-row tiles that a workgroup of expand takes together
   struct Unit* units;
   int slots;          // units that a block may have
   int splits, slice;  // workgroups that share K, steps of kStage to each
@@ -536,7 +537,7 @@ __global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = kCols * blockIdx.x + 64 * wave;
-  with_unit<FEW>(a, 16 * kTiles, [&](int adapter, int row0, int order, int count) {
+  with_unit<FEW>(a, 16 * a.tiles, [&](int adapter, int row0, int order, int count) {
     const float scale = a.scale ? a.scale[adapter] : 1.0f;
     __syncthreads();
     // 8 ranks of a row to kAdders neighbouring threads, which share the partial sums; 4 RS such
@@ -641,10 +642,13 @@ hipError_t launch_shrink(LoraArgs& a, hipStream_t st) {
 }
 template <int DT, int YT, int RS>
 hipError_t launch_expand(LoraArgs& a, hipStream_t st) {
+  // A whole unit while that occupies the chip (4096 rows of 8 adapters, R 64: 21.6 us, 26.9 a tile at a
+  // time; 256 of 24, R 16 5.4 and 6.6), else a tile (227 rows of 2 adapters, N 3797: 6.2, whole units 12.5).
+  a.tiles = mxh::cdiv(a.N, kCols) * slots_of(a.T, a.n) < 256 ? 1 : expand_tiles<YT, RS>();
   void* args[] = {&a};
   const void* f =
       a.T <= kFew ? (const void*)expand_kernel<DT, YT, RS, true> : (const void*)expand_kernel<DT, YT, RS, false>;
-  return hipLaunchKernel(f, grid_of(a, (unsigned)mxh::cdiv(a.N, kCols), 16 * expand_tiles<YT, RS>()), dim3(kThreads),
+  return hipLaunchKernel(f, grid_of(a, (unsigned)mxh::cdiv(a.N, kCols), 16 * a.tiles), dim3(kThreads),
                          args, 0, st);
 }
 size_t part_bytes(int64_t T, int64_t K, int64_t R) { return (size_t)splits_of(T, K) * (size_t)T * (size_t)R * 4; }
@@ -696,7 +700,7 @@ extern "C" int lora_add(void* y, int64_t ldy, int ytype, const void* x, int64_t 
   const int splits = splits_of(T, K);
   LoraArgs p{(uint8_t*)y, ldy, (const uint8_t*)x, ldx * 2, (const uint8_t*)a, (const uint8_t*)b, index, scale,
              (float*)workspace, (int)T, (int)N, (int)K, (int)R, (int)n,
-             (Unit*)((uint8_t*)workspace + part_bytes(T, K, R)), (int)slots_of(T, n), splits,
+             0, (Unit*)((uint8_t*)workspace + part_bytes(T, K, R)), (int)slots_of(T, n), splits,
              (int)mxh::cdiv(mxh::cdiv(K, kStage), splits)};
   const hipStream_t st = (hipStream_t)stream;
   if (xtype == MXFP4_TYPE_BF16)
