@@ -11,10 +11,10 @@
 //   T    K    N    R   n   us for the launches   what bounds it
 //   1    7168 2112 16  8   3.6 + 4.8             latency (a call takes 11 us on the host)
 //   64   7168 4096 32  24  6.7 + 5.2             latency: 12 and 7 MB
-//   777  2064 2113 24  5   3.3 + 4.9 + 7.3       latency (x fp16, y fp32)
-//   4096 7168 4096 64  8   5.2 + 16.5 + 21.4     x once at 3.6 TB/s; y in and out at 3.1, beside the
+//   777  2064 2113 24  5   3.6 + 4.9 + 7.6       latency (x fp16, y fp32)
+//   4096 7168 4096 64  8   4.9 + 16 + 21.5       x once at 3.6 TB/s; y in and out at 3.1, beside the
 //                                                partial sums, which 16 workgroups add up each
-//   4096 4096 4096 32  28  13.7 + 12.9 + 18.1    the same (adapters in any order of rows)
+//   4096 4096 4096 32  28  5.5 + 12.8 + 18.3      the same (adapters in any order of rows)
 #include <type_traits>
 
 #include "host_common.hpp"
@@ -94,13 +94,13 @@ __host__ __device__ inline int64_t slots_of(int64_t T, int64_t n) {
 }
 
 // The units of a block of rows, by rising adapter, the rows of each in an order that the indices
-// alone decide: a counting sort. A wave counts the adapters of its rows (every 16th run of 64),
-// the counts are added up over the waves, and over the adapters the units. A round of a wave takes
-// one adapter of its rows, and the rounds bound it: 777 rows in 5 spans 3.3 us (3.7 with room for
-// 4096), 900 rows of 16 adapters at random 5.1 (7.8), 2000 of 28 8.2 (12.3), 4096 of 28 13.7, in 8
-// spans 5.2. Past 64 rows it pays: 64 rows of 24 adapters, K 7168, N 4096, take 6.7 + 5.2 us
-// without it and 4.8 + 6.0 + 6.5 with it; each row of the other way is a workgroup that looks
-// through all rows.
+// alone decide: a counting sort. A wave counts the adapters of its rows (every 16th run of 64;
+// which rows of a run have the same adapter follows from a ballot for each bit of the index), the
+// counts are added up over the waves, and over the adapters the units. Latency: 777 rows of 5
+// adapters 3.6 us (4.0 with room for 4096 rows), 2000 of 28 4.2 (4.8), 4096 of 28 5.5; a round for
+// each adapter in a wave's rows instead of the ballots took 3.3, 8.2 and 13.7. Past 64 rows it pays:
+// 64 rows of 24 adapters, K 7168, N 4096, take 6.7 + 5.2 us without it and 3.4 + 6.0 + 6.5 with it;
+// but without it each row is a workgroup that looks through all rows.
 constexpr int kPlanWaves = 16;
 template <int kWords>  // runs of 64 rows to a wave
 __global__ __launch_bounds__(64 * kPlanWaves) void plan_kernel(LoraArgs a) {
@@ -113,31 +113,24 @@ __global__ __launch_bounds__(64 * kPlanWaves) void plan_kernel(LoraArgs a) {
   auto row_of = [&](int w) { return 64 * (kPlanWaves * w + wave) + l; };
   Unit* const units = a.units + (int64_t)blockIdx.x * a.slots;
   int idx[kWords], rank[kWords];
-  uint64_t todo[kWords];
 #pragma unroll
   for (int w = 0; w < kWords; ++w) idx[w] = adapter_of(a, row0 + row_of(w));
   for (int i = l; i < a.n; i += 64) before[wave][i] = 0;
-  __syncthreads();
+  const int bits = 32 - __builtin_clz(a.n - 1 | 1);
 #pragma unroll
-  for (int w = 0; w < kWords; ++w) todo[w] = __ballot(idx[w] >= 0);
-  for (;;) {
-    uint64_t any = 0;
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) any |= todo[w];
-    if (any == 0) break;
-    int adapter = 0, total = 0;
-#pragma unroll
-    for (int w = kWords - 1; w >= 0; --w)
-      if (todo[w]) adapter = __builtin_amdgcn_readlane(idx[w], __ffsll((unsigned long long)todo[w]) - 1);
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-      const bool match = idx[w] == adapter;
-      const uint64_t rows = __ballot(match);
-      todo[w] &= ~rows;
-      if (match) rank[w] = total + __popcll(rows & below);
-      total += __popcll(rows);
+  for (int w = 0; w < kWords; ++w) {
+    uint64_t same = __ballot(idx[w] >= 0);  // the run's rows with the lane's adapter
+    for (int b = 0; b < bits; ++b) {
+      const bool bit = idx[w] >> b & 1;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
     }
-    if (l == 0) before[wave][adapter] = (uint16_t)total;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a lane reads what another has written
+    if (idx[w] >= 0) {
+      const int upto = before[wave][idx[w]];
+      rank[w] = upto + __popcll(same & below);
+      if ((same & below) == 0) before[wave][idx[w]] = (uint16_t)(upto + __popcll(same));
+    }
   }
   __syncthreads();
   int units_before = 0;  // of the adapters of the rounds before
