@@ -546,7 +546,8 @@ int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const float* weigh
  *   i = index[t];  y[t] = Ty(y[t] + scale[i] * ((x[t] . A[i]^T) . B[i]^T))
  * for rows with 0 <= i < n; other rows of y are neither read nor written. Sums are
  * fp32; x . A^T is held as a sum of 16-bit pieces for the second product (two, or
- * three where y is fp32: within 2^-16 or 2^-23 of the value).
+ * three where y is fp32: within 2^-16 or 2^-23 of the value). An adapter that holds an
+ * Inf or NaN gives unspecified values in the rows that take it, and in no others.
  *   y : in/out, [T, N] of type ytype (xtype or MXFP4_TYPE_F32), row stride ldy >= N
  *       elements, aligned to its element; ldy <= 2^36.
  *   x : [T, K] of type xtype (MXFP4_TYPE_BF16 or _F16), row stride ldx >= K.

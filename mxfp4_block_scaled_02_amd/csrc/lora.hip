@@ -14,7 +14,7 @@
 //   777  2064 2113 24  5   3.6 + 4.9 + 7.6       latency (x fp16, y fp32)
 //   4096 7168 4096 64  8   4.9 + 16 + 21.5       x once at 3.6 TB/s; y in and out at 3.1, beside the
 //                                                partial sums, which 16 workgroups add up each
-//   4096 4096 4096 32  28  5.5 + 12.8 + 18.3      the same (adapters in any order of rows)
+//   4096 4096 4096 32  28  5.5 + 12.8 + 18.3     the same (adapters in any order of rows)
 #include <type_traits>
 
 #include "host_common.hpp"
@@ -99,8 +99,8 @@ __host__ __device__ inline int64_t slots_of(int64_t T, int64_t n) {
 // counts are added up over the waves, and over the adapters the units. Latency: 777 rows of 5
 // adapters 3.6 us (4.0 with room for 4096 rows), 2000 of 28 4.2 (4.8), 4096 of 28 5.5; a round for
 // each adapter in a wave's rows instead of the ballots took 3.3, 8.2 and 13.7. Past 64 rows it pays:
-// 64 rows of 24 adapters, K 7168, N 4096, take 6.7 + 5.2 us without it and 3.4 + 6.0 + 6.5 with it;
-// but without it each row is a workgroup that looks through all rows.
+// 64 rows of 24 adapters, K 7168, N 4096, take 6.7 + 5.2 us without it, and 6.0 + 6.5 beside the
+// plan with it; but without it each row is a workgroup that looks through all rows.
 constexpr int kPlanWaves = 16;
 template <int kWords>  // runs of 64 rows to a wave
 __global__ __launch_bounds__(64 * kPlanWaves) void plan_kernel(LoraArgs a) {

@@ -635,8 +635,8 @@ def moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, sc
 def pack_experts(bq: torch.Tensor, bs: torch.Tensor) -> torch.Tensor:
     """pack_B of each expert's weight: fp4x2 [E, N, K/2] and E8M0 [E, N, K/32] (contiguous uint8) -> packed uint8
     [E, pack_B_bytes(N, K)]. Row e is expert e's packed B, for moe_a16w4 and for the grouped calls alike."""
-    if bq.dim() != 3 or bs.dim() != 3 or bq.shape[0] != bs.shape[0]:
-        raise ValueError("bq must be [E, N, K/2] and bs [E, N, K/32]")
+    if bq.dim() != 3 or bs.dim() != 3 or bq.shape[0] != bs.shape[0] or bq.shape[0] < 1:
+        raise ValueError("bq must be [E, N, K/2] and bs [E, N, K/32], E at least 1")
     return torch.stack([pack_B(q, s) for q, s in zip(bq, bs)])
 
 

@@ -274,3 +274,33 @@ def test_many_rows_to_an_expert(T, H, I, E, k):
     check(x, ids, weights, w13, w2)
     ids[:, 0] = torch.arange(T, device="cuda") % E
     check(x, ids, weights, w13, w2)
+
+
+def test_a_bad_row_of_logits_shows_in_its_token_alone():
+    x, _, _, w13, w2 = layer(40, 12, 256, 128, 10, 3)
+    p13, p2 = ops.pack_experts(*w13), ops.pack_experts(*w2)
+    logits = torch.randn(12, 10, generator=gen(41), device="cuda")
+    want = ops.moe_a16w4(x, *reversed(ops.moe_route(logits, 3)), p13, p2, 128)
+    logits[4, 7], logits[9, 0] = math.nan, math.inf
+    weights, ids = ops.moe_route(logits, 3)
+    y = ops.moe_a16w4(x, ids, weights, p13, p2, 128)
+    bad = torch.zeros(12, dtype=torch.bool, device="cuda")
+    bad[[4, 9]] = True
+    assert y[bad].isnan().all()
+    ref, bound = picked.experts(x[~bad], ids[~bad], weights[~bad], picked.dequantised(*w13), picked.dequantised(*w2))
+    assert ((y[~bad].double() - ref).abs() <= bound).all() and torch.isfinite(want).all()
+
+
+def test_the_same_packed_weights_serve_the_grouped_call():
+    """Prompts' rows through the grouped product on the experts' packed weights, as the codes dequantise."""
+    g = gen(42)
+    codes, scales = weight(g, 3, 192, 256)
+    p = ops.pack_experts(codes, scales)
+    rows = [torch.randint(-4, 5, (m, 256), generator=g, device="cuda").bfloat16() for m in (5, 70, 130)]
+    for r in rows:
+        r[:, ::32] = 4.0               # every block's scale is 1, so that its values are E2M1 numbers
+    w = picked.dequantised(codes, scales)
+    for c, r, e in zip(ops.grouped_gemm(rows, list(p), 192), rows, range(3)):
+        ref = r.double() @ w[e].t()
+        bound = (256 * picked.ADD) * (r.double().abs() @ w[e].abs().t()) + picked.HALF[torch.bfloat16] * ref.abs() * 1.01
+        assert ((c.double() - ref).abs() <= bound + 2.0 ** -130).all()
