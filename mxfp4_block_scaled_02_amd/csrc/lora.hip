@@ -304,8 +304,9 @@ __device__ __forceinline__ void shrink_few(const LoraArgs& a, int adapter, int r
   }
 }
 
+// The second launch bound keeps the sums out of accumulation registers, and the moves to and from them.
 template <int DT, int RT, int U, bool FEW>
-__global__ __launch_bounds__(kThreads) void shrink_kernel(LoraArgs a) {
+__global__ __launch_bounds__(kThreads, RT == 8 ? 2 : 3) void shrink_kernel(LoraArgs a) {
   __shared__ union {
     TileSmem<RT> tile;
     mx::v4f red[kShrinkWaves][RT][64];
@@ -453,8 +454,11 @@ constexpr int expand_tiles() {  // row tiles that go together: their rows of y a
 }
 template <int DT, int YT, int RS>
 struct ExpandSmem {
-  // Ranks of a row in pieces of 8, one row 16 bytes longer than its ranks.
-  typename Half<DT>::V u[YT == MXFP4_TYPE_F32 ? 3 : 2][16 * expand_tiles<YT, RS>()][4 * RS + 1];
+  // Ranks of a row in pieces of 8, piece p of row t at p ^ swizzle(t): see TileSmem.
+  typename Half<DT>::V u[YT == MXFP4_TYPE_F32 ? 3 : 2][16 * expand_tiles<YT, RS>()][4 * RS];
+  static __device__ __forceinline__ int swizzle(int t) {
+    return RS == 1 ? 0 : RS == 2 ? t >> 1 & 7 : (t & 1) << 3 | (t & 2) << 1 | (t >> 2 & 3);
+  }
   float back[16 * expand_tiles<YT, RS>()];  // undoes the power of two
 };
 // 64 columns, from n0 on, of a unit's rows. FULL: y has all of them.
@@ -501,7 +505,7 @@ struct Columns {
 #pragma unroll
       for (int s = 0; s < RS; ++s)
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) piece[s][p] = sm.u[p][t][4 * s + g];
+        for (int p = 0; p < kPieces; ++p) piece[s][p] = sm.u[p][t][(4 * s + g) ^ sm.swizzle(t)];
       float v[16], by = scale;
       if constexpr (DT == MXFP4_TYPE_F16) by = by * sm.back[t];
       Y::unpack(held[m], v);
@@ -581,7 +585,7 @@ __global__ __launch_bounds__(kThreads, RS == 4 || (RS == 2 && YT == MXFP4_TYPE_F
               v[e] = Half<DT>::round(f[e]);
               f[e] = f[e] - (float)v[e];
             }
-            sm.u[p][t][at] = v;
+            sm.u[p][t][at ^ sm.swizzle(t)] = v;
           }
       }
     };

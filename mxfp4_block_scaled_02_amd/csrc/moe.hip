@@ -11,10 +11,10 @@
 // Measured on the MI355X (a linear read of memory reaches 5.5 to 5.8 TB/s, a copy 5.2):
 //   T   k  E   H    I     us for the launches    what bounds it
 //   1   8  32  7168 2048  21.6 + 15.2            the weights of 8 experts, 187 MB: 5.8 and 4.1 TB/s
-//   64  8  64  7168 2048  181 + 98 + 4.9         all weights, 1.50 GB: 5.5 and 5.2 TB/s
+//   64  8  64  7168 2048  181 + 98 + 4.9         all weights, 1.50 GB: 5.5 and 5.1 TB/s
 //   37  3  24  2112 1056  16.3 + 11.3 + 3.9      latency: one pass of 33 and 17 workgroups an expert
 //   124 4  6   2240 1568  42.3 + 4.6             latency: 150 and 108 workgroups for 32 rows each
-//   256 4  32  2048 1024  23 + 20.4 + 4.7        the FP4 conversions and products, about 14 us each
+//   256 4  32  2048 1024  21.9 + 20.4 + 4.7      vector instructions, 70 % of the cycles: conversions
 //   2   2  8   512  256   4.2 + 4.7              latency (a call takes 11 us on the host)
 #include "host_common.hpp"
 #include "mx_device.hpp"
@@ -310,8 +310,13 @@ __global__ __launch_bounds__(kThreads) void few_kernel(MoeArgs a) {
 // More rows to an expert, and the down product: 32 columns to a wave, activations through LDS
 // ---------------------------------------------------------------------------
 // A 128-k step of up to 64 rows lies in LDS as 16 pieces of 16 bytes to a row, piece p of row r
-// at p ^ (r % 16): the operand reads (one piece of 16 rows) and the writes (a row's pieces) hit
-// distinct banks. Two buffers, one barrier to a step. PL: the rows' parts.
+// at p ^ swizzle(r). LDS serves a wave's 16-byte accesses eight lanes at a time, four and four from
+// neighbouring groups of 16 (lanes 0 .. 3 with 20 .. 23, 4 .. 7 with 16 .. 19, ...): with the row's low
+// bits on top these hit distinct banks, in the reads (4 rows of a piece, 4 of the next group's) and in
+// the writes (4 pieces of a row, 4 of the next). p ^ (r % 16) made each read collide once (1024
+// tokens, k 4, 32 experts, H 2048, I 1024: 67 + 58 us, so 63 + 56; no difference at 256 tokens).
+// Two buffers, one barrier to a step. PL: the rows' parts.
+__device__ __forceinline__ int swizzle(int row) { return (row & 1) << 3 | (row & 2) << 1 | (row >> 2 & 3); }
 template <int MAXNT, int PL>
 struct ManySmem {
   Rows rows;
@@ -372,7 +377,7 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP>& o
 #pragma unroll
     for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
-      for (int r = 0; r < NT; ++r) sm.x[buf][pl][16 * r + (tid >> 4)][piece ^ (tid >> 4)] = v.x[pl][r];
+      for (int r = 0; r < NT; ++r) sm.x[buf][pl][16 * r + (tid >> 4)][piece ^ swizzle(tid >> 4)] = v.x[pl][r];
   };
   ManyStep<NT, PL> v[2];
   load(0, v[0]);
@@ -390,7 +395,7 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP>& o
       __builtin_amdgcn_sched_barrier(0);  // keeps the loads ahead of the products
       if (s + i < steps)
         multiply<NT, PL, 2>(code, i, [&](int r, int pl, int j) {
-          return __builtin_bit_cast(v8bf, sm.x[i][pl][16 * r + c][(4 * g + j) ^ c]);
+          return __builtin_bit_cast(v8bf, sm.x[i][pl][16 * r + c][(4 * g + j) ^ swizzle(c)]);
         }, acc);
     }
   }
@@ -411,8 +416,11 @@ __device__ __forceinline__ void many_rows(const MoeArgs& a, const Columns<UP>& o
 }
 
 // `tiles` <= MAXNT row tiles go together; the workgroups along z share an expert's rows.
+// Two waves to a SIMD are asked for, so that no more than 256 registers are there to use: with more
+// the sums would live in accumulation registers and move out and back in every step (256 tokens, k 4,
+// 32 experts, H 2048, I 1024: 21.9 us for gate and up, 23.5 that way).
 template <bool UP, int MAXNT>
-__global__ __launch_bounds__(kThreads) void many_kernel(MoeArgs a, int tiles) {
+__global__ __launch_bounds__(kThreads, 2) void many_kernel(MoeArgs a, int tiles) {
   __shared__ __align__(16) ManySmem<MAXNT, UP ? 1 : 2> sm;
   int expert = blockIdx.y;
   Codes<2> begin[2];
