@@ -14,7 +14,7 @@
 //   64  8  64  7168 2048  181 + 98 + 4.9         all weights, 1.50 GB: 5.5 and 5.1 TB/s
 //   37  3  24  2112 1056  16.3 + 11.3 + 3.9      latency: one pass of 33 and 17 workgroups an expert
 //   124 4  6   2240 1568  42.3 + 4.6             latency: 150 and 108 workgroups for 32 rows each
-//   256 4  32  2048 1024  21.9 + 20.4 + 4.7      vector instructions, 70 % of the cycles: conversions
+//   256 4  32  2048 1024  21.9 + 20.4 + 4.7      vector instructions, 60 % of the cycles: conversions
 //   2   2  8   512  256   4.2 + 4.7              latency (a call takes 11 us on the host)
 #include "host_common.hpp"
 #include "mx_device.hpp"
@@ -651,9 +651,9 @@ extern "C" int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const f
   void* args[] = {&a};
   const hipStream_t st = (hipStream_t)stream;
   const int64_t P = T * k;
-  // Rows to an expert: with 10 on average the two take the same time (H 2048, I 1024, 32 experts:
-  // gate and up 18.1 and 17.5 us), with 8 few is faster (H 4096, I 1536, 16 experts: 22.5 and
-  // 25.0), with 16 many (35.8 and 29.0: few goes over the weight again for every 16 rows).
+  // Rows to an expert: up to 10 on average few is as fast or faster (H 2048, I 1024, 32 experts: gate and up
+  // 18.6 us, many 17.9; H 4096, I 1536, 16 experts 24.4 and 26.8), with 12 many is (22.0 and 18.6; 29.9 and
+  // 26.7): few goes over the weight again for every 16 rows.
   const bool many = P > 10 * E;
   const unsigned slots = (unsigned)(P < E ? P : E), tiles = (unsigned)(I / 32);
   hipError_t e = many ? launch_many<true, 4>(a, slots, st)
