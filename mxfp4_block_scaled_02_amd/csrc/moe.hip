@@ -481,10 +481,11 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
 // 15.2 us and 15.3 + 4.4; 2 tokens, k 2, H 512, I 256 4.7 and 4.2 + 1.7; 8 tokens, k 8, H 4096,
 // I 256 17.8 and 12.9 + 3.9; beside a launch less.
 constexpr int kTokens = 16, kTokenPairs = 64;
-// Of 8 k: all pairs' I, each rounded up to 128. With 2048 at most 5 tokens, k 2, H 3392, I 1856 took
-// 12.4 + 3.9 us in the other two launches, here 11.0; 3 tokens, k 8, H 4096, I 1024 12.0 + 3.9 and 17.5.
-constexpr int kTokenPieces = 3072;
+// Of 8 k: all pairs' I, each rounded up to 128; three to a thread. With two at most, 5 tokens, k 2,
+// H 3392, I 1856 took 12.4 + 3.9 us in the other two launches, here 11.0; 3 tokens, k 8, H 4096, I 1024
+// 12.0 + 3.9 and 17.5.
 constexpr int kTokenWaves = 16;
+constexpr int kTokenPieces = 3 * 64 * kTokenWaves;
 template <int NC>
 struct TokenSmem {
   int slots;

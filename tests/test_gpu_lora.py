@@ -203,3 +203,31 @@ def test_two_captured_graphs_replayed_at_once():
                 g.replay()
         torch.cuda.synchronize()
         assert torch.equal(cases[0]["y"], want[0]) and torch.equal(cases[1]["y"], want[1])
+
+
+@pytest.mark.parametrize("T,n", [(40, 3), (400, 3), (400, 90), (5000, 40)])
+def test_calls_on_two_streams_at_once(T, n):
+    cases = [case(50 + i, T, 520, 264, 16, n, torch.bfloat16, torch.float32) for i in range(2)]
+    want = [ops.lora_add(**dict(c, y=c["y"].clone())) for c in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(ops.lora_add(**dict(cases[i], y=cases[i]["y"].clone())))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(y, w) for y in g)
+
+
+@pytest.mark.parametrize("N,n", [(255, 23), (256, 23), (24 * 256, 15), (25 * 256, 16)])
+def test_either_side_of_the_way_a_unit_is_taken(N, n):
+    """Whole units of 64 rows or a tile at a time; spans and rows in any order."""
+    for dtype, out in TYPES:
+        c = case(N + n, 64, 72, N, 24, n, dtype, out)
+        check(c)
+        c["index"][:] = n - 1
+        check(c)
+        c = case(N, 200, 72, N, 24, n, dtype, out)
+        c["index"][:] = torch.arange(200, device="cuda") // 90
+        check(c)

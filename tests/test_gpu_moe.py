@@ -304,3 +304,26 @@ def test_the_same_packed_weights_serve_the_grouped_call():
         ref = r.double() @ w[e].t()
         bound = (256 * picked.ADD) * (r.double().abs() @ w[e].abs().t()) + picked.HALF[torch.bfloat16] * ref.abs() * 1.01
         assert ((c.double() - ref).abs() <= bound + 2.0 ** -130).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 8, 8), (3, 40, 2), (16, 5, 4), (20, 40, 1), (90, 4, 1)])
+def test_no_token_has_an_expert(T, E, k):
+    x, ids, weights, w13, w2 = layer(T, T, 288, 96, E, k)
+    ids[:] = torch.tensor([-1, E, 2 ** 31 - 1, -2 ** 31], device="cuda").repeat(T * k)[: T * k].view(T, k).int()
+    out = torch.full((T, 288), math.nan, device="cuda").bfloat16()
+    assert (check(x, ids, weights, w13, w2, out=out) == 0).all()
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [layer(50 + i, T, 1024, 512, 12, 3) for i, T in enumerate((9, 100))]
+    packed = [(ops.pack_experts(*c[3]), ops.pack_experts(*c[4])) for c in cases]
+    want = [ops.moe_a16w4(*c[:3], *p, 512) for c, p in zip(cases, packed)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(ops.moe_a16w4(*cases[i][:3], *packed[i], 512))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(y, w) for y in g)
