@@ -477,7 +477,8 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
 // own: no partial products in memory, no launch to add them. The work is a list of (expert,
 // 128 k), taken in turn by the waves; h of all pairs lies in LDS, piece p (8 k) of a row of
 // token t at p ^ t, which spreads a piece of the tokens over distinct banks. A token without the
-// expert has a row of zeros. Against many_kernel and combine_kernel: one token, k 8, H 7168, I 2048
+// expert has a row of zeros, and keeps its sums: zeros times a weight that is not finite are NaN.
+// Against many_kernel and combine_kernel: one token, k 8, H 7168, I 2048
 // 15.2 us and 15.3 + 4.4; 2 tokens, k 2, H 512, I 256 4.7 and 4.2 + 1.7; 8 tokens, k 8, H 4096,
 // I 256 17.8 and 12.9 + 3.9; beside a launch less.
 constexpr int kTokens = 16, kTokenPairs = 64;
@@ -570,11 +571,18 @@ __global__ __launch_bounds__(64 * kTokenWaves) void tokens_kernel(MoeArgs a) {
     const Tile t[1] = {tile_at(p, NC == 2 ? blockIdx.x : blockIdx.x / 2)};
     Codes<NC> code;
     load_codes<NC, NC == 1>(t, s, code, blockIdx.x & 1);
-    const int pair = sm.pair[slot][c];
+    const int pair = sm.pair[slot][c];  // of the lane's token, in the operand and in the result alike
+    mx::v4f kept[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) kept[i] = acc[0][i];
     multiply<1, 2, NC>(code, s, [&](int, int pl, int j) {
       const u32x4* x = pair >= 0 ? &sm.h[pl][pair * pieces + ((16 * s + 4 * g + j) ^ c)] : &sm.zero;
       return __builtin_bit_cast(v8bf, *x);
     }, acc);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][i][e] = pair >= 0 ? acc[0][i][e] : kept[i][e];
     slot += by;
     s += rest;
     if (s >= steps) {
