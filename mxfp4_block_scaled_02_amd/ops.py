@@ -583,7 +583,10 @@ _I32, _U8, _BF16 = torch.int32, torch.uint8, torch.bfloat16
 # The library's size queries are pure functions of a few integers.
 @functools.lru_cache(maxsize=256)
 def _expert_bytes(I: int, H: int) -> tuple:
-    return int(lib().mxfp4_pack_B_bytes(2 * I, H)), int(lib().mxfp4_pack_B_bytes(H, I))
+    """Packed bytes of an expert's gate and up rows and of its down rows, and of those with the next I that takes more,
+    which a row of bytes stays below: I is not stored with the weights, and a wrong one would find others in their places."""
+    size = lib().mxfp4_pack_B_bytes
+    return int(size(2 * I, H)), int(size(H, I)), int(size(2 * I + 64, H)), int(size(H, I + 64))
 
 
 @functools.lru_cache(maxsize=256)
@@ -640,10 +643,10 @@ def pack_experts(bq: torch.Tensor, bs: torch.Tensor) -> torch.Tensor:
     return torch.stack([pack_B(q, s) for q, s in zip(bq, bs)])
 
 
-def _experts(p: torch.Tensor, name: str, need: int, N: int, K: int, dev: int):
-    """(number of experts, bytes from one to the next) of packed expert weights."""
+def _experts(p: torch.Tensor, name: str, need: int, N: int, K: int, dev: int, below: int | None = None):
+    """(number of experts, bytes from one to the next) of packed expert weights; `below`: see _expert_bytes."""
     if (p.dtype is not _U8 or p.get_device() != dev or p.dim() != 2 or need == 0 or p.shape[1] < need
-            or p.stride(1) != 1):
+            or p.stride(1) != 1 or (below is not None and p.shape[1] >= below)):
         raise ValueError(f"{name} must be uint8 [E, {need}] (pack_experts of {N} x {K}) on device {dev}, "
                          f"got {p.dtype} {list(p.shape)} on {p.device}")
     return p.shape[0], p.stride(0) if p.shape[0] > 1 else p.shape[1]
@@ -653,7 +656,8 @@ def moe_a16w4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: to
               out: torch.Tensor | None = None) -> torch.Tensor:
     """The experts' gated MLP for a few tokens: y[t] = sum_j weights[t, j] * W2_e (silu(G_e x[t]) * (U_e x[t])) with
     e = ids[t, j]; ids outside [0, E) are left out. x bf16 [T, H], ids int32 and weights float32 [T, k] (from moe_route,
-    for example), w13 and w2 from pack_experts: [E] weights of 2I x H (gate rows G, then up rows U) and of H x I.
+    for example), w13 and w2 from pack_experts: [E] weights of 2I x H (gate rows G, then up rows U) and of H x I; a row of
+    bytes may be longer than its weight by less than the next I would take (of longer ones, pass the columns in front).
     Returns bf16 [T, H], or `out`."""
     dev = x.get_device()
     if dev < 0 or x.dim() != 2:
@@ -662,19 +666,20 @@ def moe_a16w4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: to
     if ids.dim() != 2:
         raise ValueError("ids must be [T, k]")
     k, ldx = ids.shape[1], H
-    need13, need2 = _expert_bytes(I, H)
+    need13, need2, below13, below2 = _expert_bytes(I, H)
     if (x.dtype is _BF16 and ids.dtype is _I32 and weights.dtype is _F32 and w13.dtype is _U8 and w2.dtype is _U8
             and x.is_contiguous() and ids.is_contiguous() and weights.is_contiguous() and w13.is_contiguous()
             and w2.is_contiguous() and ids.get_device() == dev and weights.get_device() == dev
             and w13.get_device() == dev and w2.get_device() == dev and ids.shape[0] == T and weights.shape == ids.shape
-            and need13 and w13.dim() == 2 and w2.dim() == 2 and w13.shape[1] >= need13 and w2.shape[1] >= need2):
+            and need13 and w13.dim() == 2 and w2.dim() == 2 and need13 <= w13.shape[1] < below13
+            and need2 <= w2.shape[1] < below2):
         (E, stride13), (E2, stride2) = w13.shape, w2.shape
     else:
         ldx = _matrix(x, "x", _BF16, T, H, dev)
         _dense(ids, "ids", _I32, (T, k), dev)
         _dense(weights, "weights", _F32, (T, k), dev)
-        E, stride13 = _experts(w13, "w13", need13, 2 * I, H, dev)
-        E2, stride2 = _experts(w2, "w2", need2, H, I, dev)
+        E, stride13 = _experts(w13, "w13", need13, 2 * I, H, dev, below13)
+        E2, stride2 = _experts(w2, "w2", need2, H, I, dev, below2)
     if E != E2:
         raise ValueError(f"w13 has {E} experts and w2 {E2}")
     device = x.device

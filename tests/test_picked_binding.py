@@ -1,0 +1,58 @@
+"""What the binding of the experts' call lets through, without a GPU: the library's call is recorded, not made."""
+import pytest
+import torch
+
+from mxfp4_block_scaled_02_amd import ops
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    made = []
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(ops, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(ops, "_call", lambda fn, where, dev, args: made.append((where, args)))
+    return made
+
+
+def layer(T, H, I, E, pad13=0, pad2=0):
+    n13, n2 = ops.pack_B_bytes(2 * I, H), ops.pack_B_bytes(H, I)
+    return (torch.zeros(T, H).bfloat16(), torch.zeros(T, 2, dtype=torch.int32), torch.zeros(T, 2),
+            torch.zeros(E, n13 + pad13, dtype=torch.uint8), torch.zeros(E, n2 + pad2, dtype=torch.uint8))
+
+
+def forms(w):
+    """The same experts contiguous, and with room between them."""
+    wide = torch.zeros(w.shape[0], w.shape[1] + 64, dtype=torch.uint8)
+    return w, wide[:, :w.shape[1]]
+
+
+@pytest.mark.parametrize("H", [32, 96, 512])
+@pytest.mark.parametrize("I", [64, 96, 128, 544])
+def test_an_intermediate_size_that_the_weights_do_not_have_is_refused(calls, H, I):
+    x, ids, weights, w13, w2 = layer(3, H, I, 4)
+    for a, b in zip(forms(w13), forms(w2)):
+        for wrong in [i for i in (32, 64, 96, 128, 160, 512, 544, 576, 1024) if i != I]:
+            with pytest.raises(ValueError, match="w13 must be uint8"):
+                ops.moe_a16w4(x, ids, weights, a, b, wrong)
+        assert not calls
+        ops.moe_a16w4(x, ids, weights, a, b, I)
+        where, args = calls.pop()
+        assert where == "moe_a16w4" and args[5] == a.stride(0) and args[7] == b.stride(0) and args[14] == I
+
+
+def test_down_rows_of_another_layer_are_refused(calls):
+    x, ids, weights, w13, _ = layer(3, 96, 128, 4)
+    for other in (32, 64, 160, 192, 256):
+        w2 = layer(3, 96, other, 4)[4]
+        with pytest.raises(ValueError, match="w2 must be uint8"):
+            ops.moe_a16w4(x, ids, weights, w13, w2, 128)
+    with pytest.raises(ValueError, match="w13 has 4 experts and w2 5"):
+        ops.moe_a16w4(x, ids, weights, w13, layer(3, 96, 128, 5)[4], 128)
+    assert not calls
+
+
+def test_rows_of_bytes_may_be_longer_than_their_weight(calls):
+    x, ids, weights, w13, w2 = layer(3, 96, 128, 4, pad13=48, pad2=256)
+    ops.moe_a16w4(x, ids, weights, w13, w2, 128)
+    where, args = calls.pop()
+    assert args[5] == w13.shape[1] and args[7] == w2.shape[1]
