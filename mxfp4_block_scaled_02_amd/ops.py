@@ -213,9 +213,11 @@ def pack_B(bq: torch.Tensor, bs: torch.Tensor) -> torch.Tensor:
     K = 2 * KH
     if not (bq.is_contiguous() and bs.is_contiguous()) or bs.shape != (N, K // 32):
         raise ValueError("bq [N, K/2] and bs [N, K/32] must be contiguous and agree")
+    if bs.get_device() != bq.get_device():
+        raise ValueError("bq and bs must be on the same device")
     out = torch.empty(pack_B_bytes(N, K), dtype=torch.uint8, device=bq.device)
-    _check(lib().mxfp4_pack_B(bq.data_ptr(), bs.data_ptr(), N, K, out.data_ptr(), out.numel(), _stream(bq)),
-           "mxfp4_pack_B")
+    _call(lib().mxfp4_pack_B, "mxfp4_pack_B", bq.get_device(),
+          (bq.data_ptr(), bs.data_ptr(), N, K, out.data_ptr(), out.numel(), _stream(bq)))
     return out
 
 

@@ -56,3 +56,41 @@ def test_rows_of_bytes_may_be_longer_than_their_weight(calls):
     ops.moe_a16w4(x, ids, weights, w13, w2, 128)
     where, args = calls.pop()
     assert args[5] == w13.shape[1] and args[7] == w2.shape[1]
+
+
+def test_weights_are_packed_on_their_own_device(monkeypatch):
+    """Weights of device 1 while device 0 is current: the launch goes to device 1, and operands of two devices nowhere."""
+    current, launched = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Library:
+        mxfp4_pack_B_bytes = staticmethod(ops.lib().mxfp4_pack_B_bytes)
+
+        @staticmethod
+        def mxfp4_pack_B(*args):
+            launched.append(current[0])
+            return 0
+
+    where = {}
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: where.get(t.shape[-1], 1))
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(ops, "_current_device", lambda: current[0])
+    monkeypatch.setattr(ops, "_stream", lambda t: 0)
+    monkeypatch.setattr(ops, "lib", lambda: Library)
+    codes, scales = torch.zeros(3, 64, 48, dtype=torch.uint8), torch.zeros(3, 64, 3, dtype=torch.uint8)
+    assert ops.pack_experts(codes, scales).shape == (3, ops.pack_B_bytes(64, 96))
+    assert launched == [1, 1, 1] and current == [0]
+    where[3] = 0  # the scales, by their width
+    with pytest.raises(ValueError, match="same device"):
+        ops.pack_experts(codes, scales)
+    assert launched == [1, 1, 1]
