@@ -513,9 +513,10 @@ int moe_route(const void* logits, int64_t ldl, int dtype, const float* bias, int
  * call):
  *   for each pair (t, j) with 0 <= e = ids[t, j] < E:
  *     g = x[t] . W13[e][0..I)^T,  u = x[t] . W13[e][I..2I)^T     (fp32 sums)
- *     h = weights[t, j] * g / (1 + exp(-g)) * u                  (fp32, kept within 2^-17)
+ *     h = weights[t, j] * g / (1 + exp(-g)) * u                  (fp32, kept within 2^-17 or, if
+ *                                                                  that is less, 2^-134)
  *   y[t] = bf16(sum_j h . W2[e]^T)                               (fp32 sums)
- * MXFP4 weights dequantise to bf16 exactly for scale bytes 1 to 252; an expert with bytes
+ * MXFP4 weights dequantise to bf16 exactly for scale bytes 0 to 252; an expert with bytes
  * 253 to 255 (values past the type, NaN) gives unspecified values in the rows of y that
  * take it, and in no others. A token without a valid pair gets y = 0; the same expert
  * twice in a token counts twice. Pairs of weight 0 are computed like the others.
