@@ -641,8 +641,9 @@ template <int DT, int YT, int RS>
 hipError_t launch_expand(LoraArgs& a, hipStream_t st) {
   // A whole unit while that occupies the chip (4096 rows of 8 adapters, R 64: 21.6 us, 26.9 a tile at a
   // time; 256 of 24, R 16 5.4 and 6.6), else a tile (227 rows of 2 adapters, N 3797: 6.2, whole units 12.5;
-  // 533 of 3, N 7088, R 32 6.8 and 11.4).
-  a.tiles = mxh::cdiv(a.N, kCols) * slots_of(a.T, a.n) < 384 ? 1 : expand_tiles<YT, RS>();
+  // 533 of 3, N 7088, R 32 6.8 and 11.4). All blocks of rows count (65536 rows of 8 adapters, K and N 1024,
+  // R 32: 99 us for the call, 110 a tile at a time; 8192, R 16 20.4 and 21.4, in spans 23.3 and 23.0).
+  a.tiles = mxh::cdiv(a.N, kCols) * slots_of(a.T, a.n) * mxh::cdiv(a.T, kBlock) < 384 ? 1 : expand_tiles<YT, RS>();
   void* args[] = {&a};
   const void* f =
       a.T <= kFew ? (const void*)expand_kernel<DT, YT, RS, true> : (const void*)expand_kernel<DT, YT, RS, false>;

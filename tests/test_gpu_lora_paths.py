@@ -1,7 +1,10 @@
 """Adapters at the sizes that prompts and long rows bring: every form of the launches beside a plain form in 64 bits."""
+import ctypes
+
 import pytest
 import torch
 
+from mxfp4_block_scaled_02_amd import ops
 from tests.test_gpu_lora import TYPES, case, check
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +43,38 @@ def test_a_prompt():
 @pytest.mark.parametrize("dtype,out", TYPES)
 def test_more_rows_than_a_block_a_tile_or_a_unit_at_a_time(N, dtype, out):
     check(case(N, 9000, 40, N, 24, 8, dtype, out))
+
+
+class _Params(ctypes.Structure):
+    """hipKernelNodeParams of hip_runtime_api.h."""
+    _fields_ = [("block", ctypes.c_uint32 * 3), ("extra", ctypes.c_void_p), ("func", ctypes.c_void_p),
+                ("grid", ctypes.c_uint32 * 3), ("args", ctypes.c_void_p), ("shared", ctypes.c_uint32)]
+
+
+def grids(graph):
+    """The grids of a captured graph's kernels."""
+    with open("/proc/self/maps") as f:
+        hip = ctypes.CDLL(next(p.split()[-1] for p in f if "libamdhip64.so" in p))
+    g, n = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert hip.hipGraphGetNodes(g, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert hip.hipGraphGetNodes(g, nodes, ctypes.byref(n)) == 0
+    out = []
+    for node in nodes:
+        p = _Params()
+        assert hip.hipGraphKernelNodeGetParams(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        out.append(tuple(p.grid))
+    return out
+
+
+@pytest.mark.parametrize("T,N,z", [(4096, 512, 4), (5000, 512, 4), (8192, 512, 4), (8193, 512, 1), (9000, 513, 1), (20000, 256, 4),
+                                   (20481, 256, 1), (4096, 1536, 1), (4096, 1280, 4)])
+def test_whole_units_are_taken_once_all_blocks_of_rows_fill_the_chip(T, N, z):
+    """z workgroups of expand to a unit; 72 units to a block of 4096 rows."""
+    c = case(T, T, 8, N, 8, 8, BF, BF)
+    check(c)
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        ops.lora_add(**c)
+    blocks = -(-T // 4096)
+    assert grids(graph)[-1] == (-(-N // 256), blocks, 72 * z)
