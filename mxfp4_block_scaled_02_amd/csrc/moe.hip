@@ -478,13 +478,16 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
 // 128 k), taken in turn by the waves; h of all pairs lies in LDS, piece p (8 k) of a row of
 // token t at p ^ t, which spreads a piece of the tokens over distinct banks. A token without the
 // expert has a row of zeros, and keeps its sums: zeros times a weight that is not finite are NaN.
-// Against many_kernel and combine_kernel: one token, k 8, H 7168, I 2048
-// 15.2 us and 15.3 + 4.4; 2 tokens, k 2, H 512, I 256 4.7 and 4.2 + 1.7; 8 tokens, k 8, H 4096,
-// I 256 17.8 and 12.9 + 3.9; beside a launch less.
-constexpr int kTokens = 16, kTokenPairs = 64;
-// Of 8 k: all pairs' I, each rounded up to 128; three to a thread. With two at most, 5 tokens, k 2,
-// H 3392, I 1856 took 12.4 + 3.9 us in the other two launches, here 11.0; 3 tokens, k 8, H 4096, I 1024
-// 12.0 + 3.9 and 17.5.
+// Up to 10 pairs, past which the other two launches are as fast or faster. The call, replayed, this way and
+// with many_kernel and combine_kernel (E 32): one token, k 8, H 7168, I 2048 37.0 us and 39.4; 2 tokens,
+// k 2, H 512, I 256 7.9 and 8.7; 5 tokens, k 2, H 4096, I 1024 22.7 and 23.4, H 2048 17.0 and 16.2; 6 tokens,
+// k 2, H 2048, I 1024 18.1 and 16.5; 4 tokens, k 4, H 512, I 512 13.1 and 11.3, H 7168 26.2 and 26.8; 8
+// tokens, k 8, H 4096, I 256 27.6 and 20.7.
+constexpr int kTokens = 16;  // columns of the matrix instruction
+constexpr int kTokenPairs = 10;
+static_assert(kTokenPairs <= kTokens);
+// Of 8 k: all pairs' I, each rounded up to 128; three to a thread (5 tokens, k 2, H 3392, I 1856, which
+// needs more than two: 22.5 us this way, 25.5 the other).
 constexpr int kTokenWaves = 16;
 constexpr int kTokenPieces = 3 * 64 * kTokenWaves;
 template <int NC>
@@ -668,10 +671,10 @@ extern "C" int moe_a16w4(const void* x, int64_t ldx, const int32_t* ids, const f
   hipError_t e = many ? launch_many<true, 4>(a, slots, st)
                       : hipLaunchKernel((const void*)few_kernel, dim3(tiles, slots), dim3(kThreads), args, 0, st);
   if (e != hipSuccess) return MXFP4_ERR_HIP;
-  if (T <= kTokens && P <= kTokenPairs && P * mxh::cdiv(I, 128) * 16 <= kTokenPieces) {
-    // 16 columns to a workgroup while there is a CU for each (4 tokens, k 4, H 4096, I 1024: 256
-    // workgroups 13.2 us, 128 of 32 columns 14.6), else 32: LDS lets one workgroup to a CU (one
-    // token, k 8, H 7168, I 2048: 448 workgroups 24.3 us, 224 of 32 columns 15.2).
+  if (P <= kTokenPairs && P * mxh::cdiv(I, 128) * 16 <= kTokenPieces) {
+    // 16 columns to a workgroup while there is a CU for each (the call, replayed: 2 tokens, k 4, H 4096, I 1024,
+    // 256 workgroups 19.6 us, 128 of 32 columns 20.1), else 32: LDS lets one workgroup to a CU (H 4128: 258
+    // workgroups 26.8 us, 129 of 32 columns 20.6; one token, k 8, H 7168, I 2048 45.4 and 37.8).
     const bool narrow = H <= 16 * 256;
     const void* f = narrow ? (const void*)tokens_kernel<1> : (const void*)tokens_kernel<2>;
     const dim3 grid((unsigned)(narrow ? H / 16 : H / 32));

@@ -7,13 +7,14 @@ import torch
 
 from mxfp4_block_scaled_02_amd import ops
 from tests import picked, picked_close
+from tests.test_gpu_lora_paths import grids
 from tests.test_gpu_moe import gen, layer, weight
 
 pytestmark = pytest.mark.gpu
 
 # T, H, I, E, k: the down product by tokens with 16 and 32 columns to a workgroup; few rows to an expert; many in groups of 32
 # and of 64 rows (50 an expert on average).
-WAYS = [(5, 256, 96, 6, 2), (5, 4128, 96, 6, 2), (20, 256, 96, 30, 5), (90, 256, 96, 4, 2), (800, 928, 480, 64, 4)]
+WAYS = [(5, 256, 96, 6, 2), (5, 4128, 96, 6, 2), (6, 256, 96, 6, 2), (20, 256, 96, 30, 5), (90, 256, 96, 4, 2), (800, 928, 480, 64, 4)]
 CODE = {v: i for i, v in enumerate(picked.E2M1)}
 
 
@@ -74,7 +75,7 @@ def test_h_keeps_its_second_part(T, H, I, E, k):
 
 def one_each(E, T, way):
     """Tokens with one expert each, all of them taken: calls of (first token, tokens)."""
-    step = 16 if way == "tokens" else T
+    step = 10 if way == "tokens" else T
     return [(a, min(step, T - a)) for a in range(0, T, step)]
 
 
@@ -140,7 +141,7 @@ def test_weights_past_32_bit_offsets_on_every_way():
         assert (y[some:] == 0).all()
 
 
-@pytest.mark.parametrize("T,H,I,E,k", [(16, 256, 96, 6, 2), (40, 256, 96, 30, 3), (40, 256, 96, 3, 2)])
+@pytest.mark.parametrize("T,H,I,E,k", [(16, 256, 96, 6, 2), (10, 256, 96, 6, 1), (40, 256, 96, 30, 3), (40, 256, 96, 3, 2)])
 def test_rows_past_32_bit_offsets(T, H, I, E, k):
     """x and y with rows so far apart that the last ones lie past 2^32 bytes."""
     x, ids, weights, w13, w2 = layer(73 + E, T, H, I, E, k)
@@ -177,3 +178,24 @@ def test_one_part_of_h_differs_where_the_contract_says():
     one, _ = picked_close.experts(x, ids, w, w13, w2, parts=1)
     assert abs(y.item() - h / 2) < 1e-12 and one.item() == torch.tensor(h).bfloat16().double().item() / 2
     assert 2.0 ** -8 * h / 2 < bound.item() < 1.02 * 2.0 ** -8 * h / 2
+
+
+@pytest.mark.parametrize("T,H,I,E,k,launches", [
+    (1, 256, 96, 6, 2, 2), (5, 256, 96, 6, 2, 2), (10, 4128, 96, 12, 1, 2), (1, 64, 24576, 3, 1, 2), (1, 64, 24608, 3, 1, 3),
+    (1, 256, 96, 20, 10, 2), (1, 256, 96, 20, 11, 3), (11, 256, 96, 12, 1, 3), (4, 4128, 96, 12, 4, 3), (2, 160, 2432, 9, 5, 2),
+    (2, 160, 2464, 9, 5, 3),
+])
+def test_either_side_of_the_way_by_tokens(T, H, I, E, k, launches):
+    """Up to 10 pairs, and as much of h as there is room for, the down product adds up a token's experts itself; experts that a
+    token takes more than once, and a token without any."""
+    x, ids, weights, w13, w2 = layer(T + H + I, T, H, I, E, k)
+    d13, d2 = picked.dequantised(*w13), picked.dequantised(*w2)
+    packed = ops.pack_experts(*w13), ops.pack_experts(*w2)
+    for _ in range(3):
+        close(ops.moe_a16w4(x, ids, weights, *packed, I), *picked_close.experts(x, ids, weights, d13, d2))
+        ids[T // 2, -1], ids[-1] = -1, ids[0, 0].clone()
+        ids[0] = ids[0, 0].clone()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        ops.moe_a16w4(x, ids, weights, *packed, I)
+    assert len(grids(graph)) == launches

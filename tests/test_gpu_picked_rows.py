@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("byte", [253, 254, 255])
-@pytest.mark.parametrize("T,H,I,E,k", [(1, 256, 128, 6, 3), (7, 256, 160, 6, 2), (16, 4128, 128, 9, 3), (16, 256, 128, 9, 4),
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 256, 128, 6, 3), (5, 256, 160, 6, 2), (5, 4128, 128, 12, 2), (10, 288, 96, 7, 1), (7, 256, 160, 6, 2), (16, 4128, 128, 9, 3), (16, 256, 128, 9, 4),
                                        (17, 256, 128, 9, 2), (20, 288, 96, 30, 5), (90, 288, 96, 4, 2), (500, 1024, 96, 8, 1)])
 def test_an_expert_that_is_not_finite_changes_no_token_without_it(T, H, I, E, k, byte):
     """Both ways of the down product, and gate and up, hold tokens of several experts side by side."""
