@@ -486,8 +486,8 @@ int gemm_a8w8_path(int64_t M, int64_t N, int64_t K);
  *   score : softmax (MXFP4_SCORE_SOFTMAX) exp(l[e] - max l) / sum exp(l - max l), or
  *           sigmoid (MXFP4_SCORE_SIGMOID) 1 / (1 + exp(-l[e])), each within a few
  *           float64 roundings.
- *   rank  : l[e] without a bias, else score[e] + bias[e] in float64. An expert
- *           whose logit is -Inf, or whose rank is -Inf, is never chosen.
+ *   rank  : l[e] without a bias, else score[e] + bias[e] in float64; -Inf where the
+ *           logit is, whatever the bias. An expert whose rank is -Inf is never chosen.
  *   ids[t, 0..k)     : the experts of largest rank in falling order, equal ranks
  *           by rising index; -1 where fewer than k can be chosen.
  *   weights[t, 0..k) : fp32 of scale * score (bias not included), divided by the

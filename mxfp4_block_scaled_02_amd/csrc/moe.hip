@@ -6,7 +6,9 @@
 // are not added up in that product (tokens_kernel), their sum (combine_kernel). A workgroup has
 // some columns of one expert, finds the rows that take it in `ids` by itself, and reads its part of
 // the weight once for up to 16 (few_kernel) or 64 (many_kernel) of them: no launch sorts the rows,
-// and nothing goes back to the host.
+// and nothing goes back to the host. Up to 10 rows an expert on average one workgroup takes all of an
+// expert's rows in turns of 16, so that an expert with many more of them holds the call up (256 tokens,
+// k 8, 256 experts, H 2048, I 512: 105 us with 8 rows of each, 140 with 204 of one).
 //
 // Measured on the MI355X (a linear read of memory reaches 5.5 to 5.8 TB/s, a copy 5.2):
 //   T   k  E   H    I     us for the launches    what bounds it

@@ -7,8 +7,12 @@
 // largest rank over the wave; equal ranks go to the lowest lane, and a lane's own candidate is
 // its first, so that the lowest index wins without being compared. Reductions run over DPP
 // moves, a few cycles each; a shuffle through LDS takes over 100, and a row needs about 60 in
-// turn. That chain bounds it, not the bytes: 16 rows of 256 logits with k 8 take 5.5 us for the
-// launch (sigmoid and bias, 64-bit ranks), 4096 rows (4 MB) 6.5, 777 rows of 60 with k 3 3.4.
+// turn. 16 rows of 256 logits with k 8 take 5.4 us for the launch (sigmoid and bias, 64-bit ranks),
+// 4096 rows (4 MB) 6.4, 777 rows of 60 with k 3 3.3. Not bytes but latencies bound few rows, from
+// replays of a launch at k 1, 8 and 16: of 5.2 us 1.8 are a smallest kernel's, 1.7 the rounds (0.22 each,
+// 0.17 on 32-bit ranks), the rest the loads (each bias and each 16-bit logit is waited for by itself)
+// and the float64 scores. With 4096 rows, four waves to a SIMD, a round takes 0.29 (biased 0.41):
+// there the instructions issued count.
 #include <type_traits>
 
 #include "host_common.hpp"

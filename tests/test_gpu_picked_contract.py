@@ -199,3 +199,19 @@ def test_either_side_of_the_way_by_tokens(T, H, I, E, k, launches):
     with torch.cuda.graph(graph):
         ops.moe_a16w4(x, ids, weights, *packed, I)
     assert len(grids(graph)) == launches
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_bias_of_an_expert_out_of_use_does_not_show(score, value):
+    """The rank of a logit of -inf is -inf, whatever the expert's bias; where its logit is finite the row shows it."""
+    logits = torch.randn(9, 70, generator=gen(75), device="cuda")
+    logits[:, [3, 66]] = -math.inf
+    logits[4, 3] = 0.5
+    bias = 0.1 * torch.randn(70, generator=gen(76), device="cuda")
+    bias[3], bias[66] = value, -value
+    w, ids = ops.moe_route(logits, 8, bias=bias, score=score)
+    rw, rids = picked.route(logits.cpu(), 8, bias.cpu(), score, True, 1.0)
+    assert torch.equal(ids.cpu(), rids) and torch.equal(w.cpu().isnan(), rw.isnan())
+    assert rw.isnan().any(dim=1).tolist() == [r == 4 for r in range(9)]
+    assert ((w.cpu().double() - rw).nan_to_num(0.0).abs() <= 2.0 ** -24 * (1 + 1e-6) * rw.nan_to_num(0.0).abs()).all()
